@@ -22,10 +22,13 @@ ECHO_OUT_BF16, ECHO_OUT_F32 = 0, 1
 ECHO_STATE_F32, ECHO_STATE_BF16 = 0, 1
 ECHO_MAX_RANKS = 16
 ECHO_GROUP = 128
+ECHO_KV_BF16, ECHO_KV_F16, ECHO_KV_F32 = 0, 1, 2
 
 EXPORTED = ("echo_state_reset", "echo_quantize_feedback", "echo_owner_reduce_requant",
             "echo_dequant_gather", "echo_segment_len", "echo_codes_bytes", "echo_params_bytes",
-            "echo_state_bytes", "echo_error_string")
+            "echo_state_bytes", "echo_error_string",
+            "echo_kv_write", "echo_kv_read", "echo_kv_attention",
+            "echo_kv_codes_bytes", "echo_kv_params_bytes", "echo_kv_workspace_bytes")
 
 
 class echo_config(ctypes.Structure):
@@ -38,6 +41,24 @@ class echo_config(ctypes.Structure):
 
 class echo_seg(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("params", ctypes.c_void_p)]
+
+
+class echo_kv_cache(ctypes.Structure):
+    _fields_ = [("bits", ctypes.c_int32), ("group", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("page_size", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("num_pages", ctypes.c_int64), ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_params", ctypes.c_void_p), ("v_params", ctypes.c_void_p)]
+
+
+class echo_kv_batch(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int32), ("rows", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("max_len", ctypes.c_int32), ("table_stride", ctypes.c_int64),
+                ("row_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
+
+
+class echo_kv_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class EchoError(RuntimeError):
@@ -73,8 +94,19 @@ def load_library() -> ctypes.CDLL:
         L.echo_state_bytes.restype = ctypes.c_size_t
         L.echo_error_string.argtypes = [i32]
         L.echo_error_string.restype = ctypes.c_char_p
+        cachep, batchp, rowsp = (ctypes.POINTER(t) for t in (echo_kv_cache, echo_kv_batch, echo_kv_rows))
+        L.echo_kv_write.argtypes = [cachep, batchp, rowsp, rowsp, vp]
+        L.echo_kv_read.argtypes = [cachep, batchp, rowsp, rowsp, vp]
+        L.echo_kv_attention.argtypes = [cachep, batchp, i32, rowsp, rowsp, ctypes.c_float, i32, i32, i32,
+                                        vp, ctypes.c_size_t, vp]
+        L.echo_kv_codes_bytes.argtypes = [cachep]
+        L.echo_kv_params_bytes.argtypes = [cachep]
+        L.echo_kv_workspace_bytes.argtypes = [cachep, batchp, i32, i32, i32, i32]
+        for name in ("echo_kv_codes_bytes", "echo_kv_params_bytes", "echo_kv_workspace_bytes"):
+            getattr(L, name).restype = ctypes.c_size_t
         for name in ("echo_state_reset", "echo_quantize_feedback",
-                     "echo_owner_reduce_requant", "echo_dequant_gather"):
+                     "echo_owner_reduce_requant", "echo_dequant_gather",
+                     "echo_kv_write", "echo_kv_read", "echo_kv_attention"):
             getattr(L, name).restype = ctypes.c_int
         _LIB = L
     return _LIB
@@ -235,3 +267,209 @@ def prepare_dequant_gather(cfg: echo_config, P: int, n: int, inp, out: torch.Ten
     return Prepared(L.echo_dequant_gather,
                     (ctypes.byref(c), P, n, _seg_table(P, inp), _ptr(out), _stream(stream)),
                     (c, list(inp), out), "echo_dequant_gather")
+
+
+# ------------------------------------------------------------------ quantized K/V cache
+_KV_DTYPES = {torch.bfloat16: ECHO_KV_BF16, torch.float16: ECHO_KV_F16, torch.float32: ECHO_KV_F32}
+
+
+@dataclass
+class KVCache:
+    """A paged cache of quantized keys and values (see include/echo.h for the
+    order of the codes inside a row).  codes: uint8 [num_pages, kv_heads,
+    page_size, head_dim * bits / 8]; params: int32 words [num_pages, kv_heads,
+    page_size, head_dim / group], scale | zero << 16."""
+    bits: int
+    group: int
+    head_dim: int
+    k_codes: torch.Tensor
+    v_codes: torch.Tensor
+    k_params: torch.Tensor
+    v_params: torch.Tensor
+
+    @property
+    def num_pages(self) -> int:
+        return self.k_codes.shape[0]
+
+    @property
+    def kv_heads(self) -> int:
+        return self.k_codes.shape[1]
+
+    @property
+    def page_size(self) -> int:
+        return self.k_codes.shape[2]
+
+    @property
+    def device(self) -> torch.device:
+        return self.k_codes.device
+
+    def desc(self) -> echo_kv_cache:
+        pages, heads, slots = self.k_codes.shape[:3]
+        want = {"codes": ((pages, heads, slots, self.head_dim * self.bits // 8), torch.uint8),
+                "params": ((pages, heads, slots, self.head_dim // self.group), torch.int32)}
+        for name in ("k_codes", "v_codes", "k_params", "v_params"):
+            t = getattr(self, name)
+            shape, dtype = want[name[2:]]
+            if tuple(t.shape) != shape or t.dtype != dtype or t.device != self.device:
+                raise ValueError(f"{name}: expected {dtype} {shape} on {self.device}, "
+                                 f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+        return echo_kv_cache(self.bits, self.group, self.head_dim, heads, slots, 0, pages, _ptr(self.k_codes),
+                             _ptr(self.v_codes), _ptr(self.k_params), _ptr(self.v_params))
+
+
+@dataclass
+class KVBatch:
+    """The rows of one call: sequence b has rows row_start[b] .. row_start[b + 1] - 1
+    of the packed arrays, its last positions of kv_len[b]; page_table [seqs,
+    entries] names their pages.  All int32 on the GPU.  rows: rows of the packed
+    arrays; max_new, max_len: upper bounds of a sequence's rows and length."""
+    row_start: torch.Tensor
+    kv_len: torch.Tensor
+    page_table: torch.Tensor
+    rows: int
+    max_new: int
+    max_len: int
+
+    def desc(self, device: torch.device) -> echo_kv_batch:
+        seqs = self.kv_len.numel()
+        if self.page_table.dim() != 2 or self.page_table.shape[0] != seqs or self.row_start.shape != (seqs + 1,) \
+                or self.kv_len.dim() != 1:
+            raise ValueError("a batch is row_start [seqs + 1], kv_len [seqs] and page_table [seqs, entries]")
+        for t in (self.row_start, self.kv_len, self.page_table):
+            if t.dtype != torch.int32 or t.device != device:
+                raise ValueError(f"a batch's arrays are int32 on the cache's device {device}")
+        return echo_kv_batch(seqs, self.rows, self.max_new, self.max_len, self.page_table.shape[1],
+                             _ptr(self.row_start), _ptr(self.kv_len), _ptr(self.page_table))
+
+
+def _kv_form(num_pages, page_size, kv_heads, head_dim, bits, group) -> echo_kv_cache:
+    return echo_kv_cache(bits, group, head_dim, kv_heads, page_size, 0, num_pages, None, None, None, None)
+
+
+def echo_kv_codes_bytes(num_pages: int, page_size: int, kv_heads: int, head_dim: int, bits: int = 4,
+                        group: int = ECHO_GROUP) -> int:
+    return load_library().echo_kv_codes_bytes(ctypes.byref(
+        _kv_form(num_pages, page_size, kv_heads, head_dim, bits, group)))
+
+
+def echo_kv_params_bytes(num_pages: int, page_size: int, kv_heads: int, head_dim: int, bits: int = 4,
+                         group: int = ECHO_GROUP) -> int:
+    return load_library().echo_kv_params_bytes(ctypes.byref(
+        _kv_form(num_pages, page_size, kv_heads, head_dim, bits, group)))
+
+
+def alloc_kv_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int, bits: int = 4,
+                   group: int = ECHO_GROUP, device="cuda") -> KVCache:
+    if echo_kv_codes_bytes(num_pages, page_size, kv_heads, head_dim, bits, group) == 0:
+        raise ValueError(f"no cache of {num_pages} pages of {page_size} slots, {kv_heads} heads of {head_dim} "
+                         f"elements at {bits} bits in groups of {group}")
+    lead = (num_pages, kv_heads, page_size)
+    codes = [torch.empty(*lead, head_dim * bits // 8, dtype=torch.uint8, device=device) for _ in "kv"]
+    params = [torch.empty(*lead, head_dim // group, dtype=torch.int32, device=device) for _ in "kv"]
+    return KVCache(bits, group, head_dim, *codes, *params)
+
+
+def _kv_rows(t: torch.Tensor, what: str, rows: int, heads: int, head_dim: int, device: torch.device) -> echo_kv_rows:
+    if tuple(t.shape) != (rows, heads, head_dim) or t.device != device or t.dtype not in _KV_DTYPES:
+        raise ValueError(f"{what}: expected bf16, fp16 or fp32 rows ({rows}, {heads}, {head_dim}) on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.numel() and t.stride(2) != 1:
+        raise ValueError(f"{what}: the elements of a row must be contiguous")
+    return echo_kv_rows(t.data_ptr() or None, t.stride(0), t.stride(1), _KV_DTYPES[t.dtype], 0)
+
+
+class _PreparedOn(Prepared):
+    """A prepared call of tensors on one device: made with that device current,
+    whichever device the caller has current."""
+
+    def __init__(self, fn, args, keep, where: str, device: torch.device):
+        super().__init__(fn, args, keep, where)
+        self._device = device.index
+
+    def __call__(self):
+        if torch.cuda.current_device() == self._device:
+            return super().__call__()
+        with torch.cuda.device(self._device):
+            return super().__call__()
+
+
+def _kv_call(cache: KVCache, batch: KVBatch, stream):
+    device = cache.device
+    if device.type != "cuda":
+        raise ValueError("the cache must be on a GPU")
+    st = torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream)
+    return device, cache.desc(), batch.desc(device), st
+
+
+def _prepare_kv_rows(fn, where: str, cache: KVCache, batch: KVBatch, k, v, stream) -> Prepared:
+    device, c, b, st = _kv_call(cache, batch, stream)
+    kr, vr = (_kv_rows(t, n, batch.rows, cache.kv_heads, cache.head_dim, device) for t, n in ((k, "k"), (v, "v")))
+    return _PreparedOn(fn, (ctypes.byref(c), ctypes.byref(b), ctypes.byref(kr), ctypes.byref(vr), st),
+                       (c, b, kr, vr, cache, batch, k, v), where, device)
+
+
+def prepare_kv_write(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream=None) -> Prepared:
+    return _prepare_kv_rows(load_library().echo_kv_write, "echo_kv_write", cache, batch, k, v, stream)
+
+
+def prepare_kv_read(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream=None) -> Prepared:
+    return _prepare_kv_rows(load_library().echo_kv_read, "echo_kv_read", cache, batch, k, v, stream)
+
+
+def echo_kv_workspace_bytes(cache: KVCache, batch: KVBatch, q_heads: int, causal=True, window: int = 0,
+                            sinks: int = 0) -> int:
+    c, b = cache.desc(), batch.desc(cache.device)
+    return load_library().echo_kv_workspace_bytes(ctypes.byref(c), ctypes.byref(b), q_heads, int(causal), window,
+                                                  sinks)
+
+
+def prepare_kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, out: torch.Tensor, scale: float,
+                         causal=True, window: int = 0, sinks: int = 0, workspace: torch.Tensor | None = None,
+                         stream=None) -> Prepared:
+    """workspace: uint8, at least echo_kv_workspace_bytes(); by default one of
+    the prepared call's own.  Calls that may run at the same time (other
+    streams, graphs replayed side by side) must not share one."""
+    device, c, b, st = _kv_call(cache, batch, stream)
+    q_heads = q.shape[1] if q.dim() == 3 else 0
+    qr, outr = (_kv_rows(t, n, batch.rows, q_heads, cache.head_dim, device) for t, n in ((q, "q"), (out, "out")))
+    if workspace is None:
+        workspace = torch.empty(echo_kv_workspace_bytes(cache, batch, q_heads, causal, window, sinks),
+                                dtype=torch.uint8, device=device)
+    elif workspace.dtype != torch.uint8 or workspace.device != device:
+        raise ValueError(f"workspace: uint8 on {device}")
+    return _PreparedOn(load_library().echo_kv_attention,
+                       (ctypes.byref(c), ctypes.byref(b), q_heads, ctypes.byref(qr), ctypes.byref(outr), scale,
+                        int(causal), window, sinks, _ptr(workspace) or None, workspace.numel(), st),
+                       (c, b, qr, outr, cache, batch, q, out, workspace), "echo_kv_attention", device)
+
+
+def echo_kv_write(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream=None):
+    """k, v: [rows, kv_heads, head_dim], bf16, fp16 or fp32, any strides of 16-byte multiples."""
+    prepare_kv_write(cache, batch, k, v, stream)()
+
+
+def echo_kv_read(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream=None):
+    """k, v: [rows, kv_heads, head_dim] to fill, bf16, fp16 or fp32."""
+    prepare_kv_read(cache, batch, k, v, stream)()
+
+
+def echo_kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, out: torch.Tensor, scale: float,
+                      causal=True, window: int = 0, sinks: int = 0, workspace: torch.Tensor | None = None,
+                      stream=None):
+    """q, out: [rows, q_heads, head_dim], both bf16 or both fp16.  Without a
+    workspace one is allocated for this call on its stream."""
+    if workspace is None:
+        with torch.cuda.stream(_as_stream(cache.device, stream)):
+            workspace = torch.empty(echo_kv_workspace_bytes(cache, batch, q.shape[1], causal, window, sinks),
+                                    dtype=torch.uint8, device=cache.device)
+    prepare_kv_attention(cache, batch, q, out, scale, causal, window, sinks, workspace, stream)()
+
+
+def _as_stream(device: torch.device, stream):
+    """torch's object for a stream argument: memory allocated under it may be
+    reused once the stream's work is done."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if hasattr(stream, "cuda_stream"):
+        return stream
+    return torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)

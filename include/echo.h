@@ -187,6 +187,118 @@ size_t echo_codes_bytes(int64_t seg_len, int bits);
 size_t echo_params_bytes(int64_t seg_len, int group);
 size_t echo_state_bytes(int64_t n, int state_dtype);
 
+/*
+ * Quantized K/V cache: keys and values of attention in 4- or 8-bit codes with
+ * the quantizer above (group minimum as fp16 zero point, fp16 step, codes round
+ * half to even, value = fma(code, step, zero)), written row by row, read back,
+ * and read by an attention that works on the codes.
+ *
+ * The row of one token and K/V head is head_dim elements in groups of `group`.
+ * Four arrays hold the cache, codes[num_pages][kv_heads][page_size][head_dim *
+ * bits / 8] bytes and params[num_pages][kv_heads][page_size][head_dim / group]
+ * words (scale | zero << 16) for keys and for values.  Inside a row the codes
+ * are in the order in which the attention kernel's lanes take them: keys as
+ * their 8-element runs, run 4 w + i at place i * head_dim / 32 + w; values with
+ * element 16 i + m at place m * head_dim / 16 + i; of two 4-bit codes in a byte
+ * the earlier place is in the low nibble.  A cache needs no initialization.
+ *
+ * A call works on the rows of several sequences, packed one after the other:
+ * sequence b has the rows row_start[b] .. row_start[b + 1] - 1, and they are its
+ * LAST positions: with n = row_start[b + 1] - row_start[b], row i of the n sits
+ * at position kv_len[b] - n + i, in slot position % page_size of the page
+ * page_table[b * table_stride + position / page_size].  The same description
+ * serves writing a step's rows, attending with its queries, and reading rows.
+ *
+ * The three device arrays cannot be checked by the host.  Whatever they hold,
+ * no call leaves the caller's buffers: a row outside every sequence, a position
+ * below 0, from max_len on or past the page table, and an entry that names no
+ * page are passed over (not written, not read, not attended to).  Rows behind
+ * the last sequence keep their contents.  Two rows of one call in the same slot
+ * (a page in two places of the table) leave that slot undefined.
+ */
+typedef struct echo_kv_cache {
+    int32_t   bits;         /* 4 or 8 */
+    int32_t   group;        /* 32, 64 or 128, at most head_dim */
+    int32_t   head_dim;     /* 64, 128 or 256 */
+    int32_t   kv_heads;     /* 1 .. 4096 */
+    int32_t   page_size;    /* slots of a page: 16, 32, 64, 128 or 256 */
+    int32_t   reserved;     /* not read */
+    int64_t   num_pages;    /* 1 .. 2^31 - 1 */
+    void*     k_codes;      /* echo_kv_codes_bytes() each */
+    void*     v_codes;
+    uint32_t* k_params;     /* echo_kv_params_bytes() each */
+    uint32_t* v_params;
+} echo_kv_cache;
+
+typedef struct echo_kv_batch {
+    int32_t seqs;                /* sequences, at most 65535 */
+    int32_t rows;                /* rows of the packed arrays, at most 2^30 */
+    int32_t max_new;             /* no sequence has more rows (attention: later ones are not computed) */
+    int32_t max_len;             /* no kv_len is larger (a larger one is cut to it) */
+    int64_t table_stride;        /* page-table entries per sequence */
+    const int32_t* row_start;    /* device, seqs + 1, ascending */
+    const int32_t* kv_len;       /* device, seqs: positions in use, this call's rows included */
+    const int32_t* page_table;   /* device, seqs * table_stride */
+} echo_kv_batch;
+
+/* Packed rows [rows, heads, head_dim], head_dim contiguous, strides in elements.
+ * Every row is 16-byte aligned; rows that are written share no element. */
+#define ECHO_KV_BF16     0
+#define ECHO_KV_F16      1
+#define ECHO_KV_F32      2
+typedef struct echo_kv_rows {
+    void*   data;
+    int64_t row_stride;
+    int64_t head_stride;
+    int32_t dtype;          /* ECHO_KV_* */
+    int32_t reserved;       /* not read */
+} echo_kv_rows;
+
+/*
+ * echo_kv_write -- quantize the batch's rows of keys and values into the cache.
+ *   k, v: [rows, kv_heads, head_dim], the same type (bf16, fp16 or fp32).
+ *   NaN becomes code 0; an infinity the end of the group's range.
+ *   Errors: ECHO_ERR_ARG, ECHO_ERR_SHAPE, ECHO_ERR_ALIGN, ECHO_ERR_HIP.
+ */
+int echo_kv_write(const echo_kv_cache* cache, const echo_kv_batch* batch,
+                  const echo_kv_rows* k, const echo_kv_rows* v, void* stream);
+
+/*
+ * echo_kv_read -- the batch's rows of keys and values as bf16, fp16 (rounded to
+ *   nearest even) or fp32.  Rows the call passes over keep their contents.
+ *   Errors: ECHO_ERR_ARG, ECHO_ERR_SHAPE, ECHO_ERR_ALIGN, ECHO_ERR_HIP.
+ */
+int echo_kv_read(const echo_kv_cache* cache, const echo_kv_batch* batch,
+                 const echo_kv_rows* k, const echo_kv_rows* v, void* stream);
+
+/*
+ * echo_kv_attention -- out = softmax(scale * q K^T) V over the cache.
+ *   q, out: [rows, q_heads, head_dim], both bf16 or both fp16; query head h
+ *   reads K/V head h / (q_heads / kv_heads).  The row at position p sees the
+ *   keys j < kv_len[b]; with causal = 1 only j <= p; with window > 0 (causal
+ *   only) of these only p - j < window or j < sinks.  A row that sees nothing
+ *   becomes 0.  scale: finite.
+ *   Scores, the softmax and sums are binary32 on the unrounded cached values;
+ *   probabilities enter the second product in fp16, relative to the row's
+ *   maximum.
+ *   workspace: echo_kv_workspace_bytes() bytes (may be NULL if that is 0), not
+ *   used by another call at the same time; its contents do not matter.
+ *   Errors: ECHO_ERR_ARG (also a workspace too small), ECHO_ERR_SHAPE,
+ *   ECHO_ERR_ALIGN, ECHO_ERR_HIP.
+ */
+int echo_kv_attention(const echo_kv_cache* cache, const echo_kv_batch* batch, int q_heads,
+                      const echo_kv_rows* q, const echo_kv_rows* out, float scale,
+                      int causal, int window, int sinks,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* Sizes (0 for invalid input): one codes array and one params array of a cache
+ * (its pointers are not read), and the workspace of an attention call (its
+ * device arrays are not read; it depends on the sizes only). */
+size_t echo_kv_codes_bytes(const echo_kv_cache* cache);
+size_t echo_kv_params_bytes(const echo_kv_cache* cache);
+size_t echo_kv_workspace_bytes(const echo_kv_cache* cache, const echo_kv_batch* batch, int q_heads,
+                               int causal, int window, int sinks);
+
 /* Static description of an error code. */
 const char* echo_error_string(int code);
 
