@@ -43,8 +43,8 @@ namespace kv {
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
-constexpr float kSlack = 4.0f;       // log2 of how far a score may exceed the running maximum
-constexpr int kStepTop = 11;         // normalised value steps stay at or below 2^11, products below 2^15
+constexpr float kPeak = 10.0f;    // a probability of 1 at the running maximum enters the products as 2^10
+constexpr float kSlack = 4.0f;    // log2 of how far a score may exceed the running maximum
 
 __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -57,8 +57,9 @@ __device__ __forceinline__ f16x8 operand(uint32_t a, uint32_t b, uint32_t c, uin
 // What one step loads: keys and values of 2 x 16 tokens and their parameters.
 template <int BITS, int D, int G>
 struct Tile {
-  static constexpr int kKeyWords = D * BITS / 32 / 4;    // words of a lane's share of one key row
-  static constexpr int kUnitBytes = D * BITS / 8 / 16;   // bytes of a lane's share of one value row
+  static constexpr int kRowBytes = D * BITS / 8;
+  static constexpr int kKeyWords = kRowBytes / 16;       // words of a lane's share of one key row
+  static constexpr int kUnitBytes = kRowBytes / 16;      // bytes of a lane's share of one value row
   static constexpr int kUnitWords = kUnitBytes < 4 ? 1 : kUnitBytes / 4;
   static constexpr int kGroups = D / G;
   uint32_t k[2][kKeyWords];
@@ -68,33 +69,34 @@ struct Tile {
 };
 
 template <int WORDS>
-__device__ __forceinline__ void load_words(const uint32_t* __restrict__ p, uint32_t* w) {
+__device__ __forceinline__ void load_words(const uint8_t* __restrict__ p, uint32_t* w) {
   if constexpr (WORDS >= 4) {
 #pragma unroll
     for (int i = 0; i < WORDS; i += 4) {
-      const u32x4 a = *reinterpret_cast<const u32x4*>(p + i);
+      const u32x4 a = *reinterpret_cast<const u32x4*>(p + 4 * i);
       w[i] = a.x, w[i + 1] = a.y, w[i + 2] = a.z, w[i + 3] = a.w;
     }
   } else if constexpr (WORDS == 2) {
     const u32x2 a = *reinterpret_cast<const u32x2*>(p);
     w[0] = a.x, w[1] = a.y;
   } else {
-    w[0] = *p;
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
   }
 }
 
-// Pages of the two halves of the tile at token tb: -1 where there is none.
+// Pages of the two halves of the tile at token tb, -1 where there is none: the
+// same in all lanes, so they are scalar loads.
 struct Pages {
-  int64_t p[2];
+  int p[2];
 };
-__device__ __forceinline__ Pages tile_pages(const KvCache& c, const int32_t* __restrict__ table,
-                                            int len, int tb) {
+__device__ __forceinline__ Pages tile_pages(const KvCache& c, const int32_t* table, int len, int tb) {
+  typedef const int32_t __attribute__((address_space(4))) * scalar_ptr;
   Pages r;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     const int t = tb + 16 * s;
-    int64_t page = -1;
-    if (t < len) page = table[t >> c.page_shift];
+    int page = -1;
+    if (t < len) page = ((scalar_ptr)(uintptr_t)table)[t >> c.page_shift];
     r.p[s] = page >= 0 && page < c.num_pages ? page : -1;
   }
   return r;
@@ -104,7 +106,10 @@ template <int BITS, int D, int G>
 __device__ __forceinline__ void load_tile(Tile<BITS, D, G>& x, const KvCache& c, const Pages& pages,
                                           int hk, int tb) {
   using T = Tile<BITS, D, G>;
-  const int n = threadIdx.x % 16, quad = threadIdx.x / 16 % 4;
+  const uint32_t n = threadIdx.x % 16, quad = threadIdx.x / 16 % 4;
+  const uint32_t k_at = n * T::kRowBytes + quad * (T::kRowBytes / 4);
+  const uint32_t v_at = quad * 4 * T::kRowBytes + n * T::kUnitBytes;
+  const uint32_t p_at = quad * 16 * T::kGroups;
   x.ok = 0;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
@@ -112,17 +117,18 @@ __device__ __forceinline__ void load_tile(Tile<BITS, D, G>& x, const KvCache& c,
     const int64_t page = pages.p[s] < 0 ? 0 : pages.p[s];
     x.ok |= pages.p[s] < 0 ? 0u : 1u << s;
     const int64_t row = ((page * c.kv_heads + hk) << c.page_shift) + ((tb + 16 * s) & ((1 << c.page_shift) - 1));
-    const uint8_t* kc = c.k_codes + row * (D * BITS / 8);
-    const uint8_t* vc = c.v_codes + row * (D * BITS / 8);
-    load_words<T::kKeyWords>(reinterpret_cast<const uint32_t*>(kc + n * (D * BITS / 8) + quad * (D * BITS / 32)), x.k[s]);
+    const uint8_t* kc = c.k_codes + row * T::kRowBytes;
+    const uint8_t* vc = c.v_codes + row * T::kRowBytes;
+    const uint8_t* kp = reinterpret_cast<const uint8_t*>(c.k_params) + row * (4 * T::kGroups);
+    const uint8_t* vp = reinterpret_cast<const uint8_t*>(c.v_params) + row * (4 * T::kGroups);
+    load_words<T::kKeyWords>(kc + k_at, x.k[s]);
+    load_words<4 * T::kGroups>(kp + p_at, &x.kp[s][0][0]);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const uint8_t* u = vc + (quad * 4 + r) * (D * BITS / 8) + n * T::kUnitBytes;
-      if constexpr (T::kUnitBytes == 2) x.v[s][r][0] = *reinterpret_cast<const uint16_t*>(u);
-      else load_words<T::kUnitWords>(reinterpret_cast<const uint32_t*>(u), x.v[s][r]);
+      if constexpr (T::kUnitBytes == 2) x.v[s][r][0] = *reinterpret_cast<const uint16_t*>(vc + v_at + r * T::kRowBytes);
+      else load_words<T::kUnitWords>(vc + v_at + r * T::kRowBytes, x.v[s][r]);
     }
-    load_words<4 * T::kGroups>(c.k_params + (row + quad * 4) * T::kGroups, &x.kp[s][0][0]);
-    load_words<4 * T::kGroups>(c.v_params + (row + quad * 4) * T::kGroups, &x.vp[s][0][0]);
+    load_words<4 * T::kGroups>(vp + p_at, &x.vp[s][0][0]);
   }
 }
 
@@ -141,12 +147,22 @@ __device__ __forceinline__ f16x8 key_operand(const uint32_t* k, int w) {
   }
 }
 
-// Operands of value tiles i and (4 bits) i + 1 from byte `byte` of the lane's
-// shares of 8 tokens: the codes of two tokens side by side.
+// Byte `byte` of the shares of two tokens, side by side in half words.
 template <int WORDS>
 __device__ __forceinline__ uint32_t byte_pair(const uint32_t (&a)[WORDS], const uint32_t (&b)[WORDS], int byte) {
   const uint32_t sel = 0x0c000c00u | (uint32_t)(byte % 4) | (uint32_t)(4 + byte % 4) << 16;
   return __builtin_amdgcn_perm(b[byte / 4], a[byte / 4], sel);
+}
+
+// (c - half) 2^-9 of two codes that lie in the low bits (SHIFT = 0) or one
+// nibble higher (SHIFT = 4) of half words: exact, and normal numbers, which
+// the matrix instruction adds up without loss.
+template <int BITS, int SHIFT>
+__device__ __forceinline__ uint32_t centred(uint32_t codes) {
+  const _Float16 up = (_Float16)(SHIFT ? 0x1p11f : 0x1p15f);
+  const _Float16 mid = (_Float16)(BITS == 4 ? -8.0f / 512 : -128.0f / 512);
+  const f16x2 v = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, codes), f16x2{up, up}, f16x2{mid, mid});
+  return __builtin_bit_cast(uint32_t, v);
 }
 
 __device__ __forceinline__ void store_out4(const KvRows& out, int64_t e, f32x4 v) {
@@ -161,6 +177,7 @@ __device__ __forceinline__ void store_out4(const KvRows& out, int64_t e, f32x4 v
   *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out.p) + e) = w;
 }
 
+// The state of a wave: 16 NT query rows against the keys seen so far.
 template <int BITS, int D, int G, int NT>
 struct Wave {
   static constexpr int kSlices = D / 32, kTiles = D / 16, kGroups = D / G;
@@ -169,11 +186,12 @@ struct Wave {
   float qs[NT][kGroups];         // sum of a row's q over a group, * 2^-24
   float rf[NT];                  // raw score -> log2 units
   int lo[NT], hi[NT];            // visible keys: j <= hi and (j >= lo or j < sinks)
-  f32x4 o[NT][kTiles];           // sum of p' c 2^-24 (2^-20 in odd tiles at 4 bits)
-  f32x4 hs[NT][kGroups];         // kHalf * sum of p' 2^-24, the same in all four
-  float m[NT], l[NT];            // running maximum (log2), this lane's part of the sum
-  float zc[NT][kGroups];         // this lane's part of sum p (zero + kHalf step)
-  float einv, elim;              // p' = p step einv while every step <= elim
+  f32x4 o[NT][kTiles];           // sum of p step einv (c - kHalf) 2^-9
+  f32x4 st[NT];                  // rows of the 16x16 result: 0 sum p; 1 + g sum p zero; 1 + kGroups + g sum p step
+  float mb[NT];                  // running maximum (log2) - kPeak
+  float einv, elim;              // einv: a power of two with step einv <= 1 while every step <= elim
+  uint32_t psel, por;            // how this lane builds its row of the operand that gives `st`
+  int pgroup;
 
   // The rows base .. base + 16 NT - 1 of a (sequence, K/V head) with `rows` rows.
   __device__ __forceinline__ void begin(const KvAttnArgs& a, const Seq& sq, int hk, int base, int rows) {
@@ -236,20 +254,21 @@ struct Wave {
         qs[t][g] += __shfl_xor(qs[t][g], 16);
         qs[t][g] += __shfl_xor(qs[t][g], 32);
         qs[t][g] *= 0x1p-24f;
-        zc[t][g] = 0.0f;
-        hs[t][g] = f32x4{0, 0, 0, 0};
       }
+      st[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int i2 = 0; i2 < kTiles; ++i2) o[t][i2] = f32x4{0, 0, 0, 0};
-      m[t] = kLowest;
-      l[t] = 0.0f;
+      mb[t] = kLowest;
     }
     einv = 1.0f;
     elim = 0.0f;
+    psel = n >= 1 && n <= kGroups ? 0x07060302u : n > kGroups && n <= 2 * kGroups ? 0x05040100u : 0x0c0c0c0cu;
+    por = n == 0 ? 0x3c003c00u : 0u;
+    pgroup = n > kGroups ? n - kGroups - 1 : n - 1;
   }
 
-  template <bool MASK>
-  __device__ __forceinline__ void step(const Tile<BITS, D, G>& x, int tb, int len, int sinks) {
+  // One tile of 32 keys at token tb; masked: some of them some row may not see.
+  __device__ __forceinline__ void step(Tile<BITS, D, G>& x, int tb, bool masked, int len, int sinks) {
     const int quad = threadIdx.x / 16 % 4;
     float sc[NT][2][4];
 #pragma unroll
@@ -267,64 +286,89 @@ struct Wave {
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float st = f16_to_f32(x.kp[s][r][g] & 0xffffu), ze = f16_to_f32(x.kp[s][r][g] >> 16);
+          const float ks = f16_to_f32(x.kp[s][r][g] & 0xffffu), kz = f16_to_f32(x.kp[s][r][g] >> 16);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            const float z = g == 0 ? ze * qs[t][g] : fmaf(ze, qs[t][g], sc[t][s][r]);
-            sc[t][s][r] = fmaf(st, acc[t][r], z);
+            const float z = g == 0 ? kz * qs[t][g] : fmaf(kz, qs[t][g], sc[t][s][r]);
+            sc[t][s][r] = fmaf(ks, acc[t][r], z);
           }
         }
       }
     }
-    float st[2][4][kGroups], ze[2][4][kGroups];
-    float top_step = 0.0f;
-    bool above = false;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int j = tb + 16 * s + quad * 4 + r;
-        const bool there = !MASK || (j < len && (x.ok >> s & 1u));
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          const uint32_t w = there ? x.vp[s][r][g] : 0u;   // slots behind the last key hold anything
-          st[s][r][g] = f16_to_f32(w & 0xffffu);
-          ze[s][r][g] = f16_to_f32(w >> 16);
-          top_step = fmaxf(top_step, st[s][r][g]);
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float v = sc[t][s][r] * rf[t];
-          if (MASK) v = there && j <= hi[t] && (j >= lo[t] || j < sinks) ? v : -INFINITY;
-          sc[t][s][r] = v;
-          above |= v > m[t] + kSlack;
-        }
-      }
-    }
-    if (__any(above || top_step > elim)) rescale(sc, top_step);
-    f16x8 pv[NT][kGroups];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    if (masked) {
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float p = __builtin_amdgcn_exp2f(sc[t][s][r] - m[t]);
-          l[t] += p;
+          const int j = tb + 16 * s + quad * 4 + r;
+          const bool there = j < len && (x.ok >> s & 1u);
 #pragma unroll
-          for (int g = 0; g < kGroups; ++g) {
-            zc[t][g] = fmaf(p, fmaf(kHalf, st[s][r][g], ze[s][r][g]), zc[t][g]);
-            pv[t][g][4 * s + r] = (_Float16)(p * (st[s][r][g] * einv));
-          }
+          for (int g = 0; g < kGroups; ++g)
+            if (!there) x.vp[s][r][g] = 0u;   // slots behind the last key hold anything
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            if (!(there && j <= hi[t] && (j >= lo[t] || j < sinks))) sc[t][s][r] = rf[t] < 0.0f ? INFINITY : -INFINITY;
         }
     }
-    // kHalf * sum of the rounded products: the same rounding as in the sums it corrects
-    const uint32_t half2 = BITS == 4 ? 0x00080008u : 0x00800080u;
-    const f16x8 halves = operand(half2, half2, half2, half2);
+    float y[NT][2][4], vs[2][4][kGroups];
+    float top_y = -INFINITY, top_step = 0.0f;
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) hs[t][g] = mfma(halves, pv[t][g], hs[t][g]);
+      for (int r = 0; r < 4; ++r) {
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          vs[s][r][g] = f16_to_f32(x.vp[s][r][g] & 0xffffu);
+          top_step = fmaxf(top_step, vs[s][r][g]);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          y[t][s][r] = fmaf(sc[t][s][r], rf[t], -mb[t]);
+          top_y = fmaxf(top_y, y[t][s][r]);
+        }
+      }
+    if (__any(top_y > kPeak + kSlack || top_step > elim)) {
+      rescale(sc, top_step);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) y[t][s][r] = fmaf(sc[t][s][r], rf[t], -mb[t]);
+    }
+    // the operand of the sums that need no code: row 0 ones, then zeros, then steps
+    uint32_t sw[2][4];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        sw[s][r] = x.vp[s][r][0];
+#pragma unroll
+        for (int g = 1; g < kGroups; ++g) sw[s][r] = pgroup == g ? x.vp[s][r][g] : sw[s][r];
+      }
+    auto pick = [&](int s, int r) { return __builtin_amdgcn_perm(sw[s][r + 1], sw[s][r], psel) | por; };
+    const f16x8 sums = operand(pick(0, 0), pick(0, 2), pick(1, 0), pick(1, 2));
+    f16x8 pv[NT][kGroups];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) vs[s][r][g] *= einv;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      f16x8 p;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float e = __builtin_amdgcn_exp2f(y[t][s][r]);
+          p[4 * s + r] = (_Float16)e;
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) pv[t][g][4 * s + r] = (_Float16)(e * vs[s][r][g]);
+        }
+      st[t] = mfma(sums, p, st[t]);
+    }
 #pragma unroll
     for (int byte = 0; byte < kTiles * BITS / 8; ++byte) {
       uint32_t c[4];
@@ -334,15 +378,18 @@ struct Wave {
         c[2 * s + 1] = byte_pair(x.v[s][2], x.v[s][3], byte);
       }
       if constexpr (BITS == 4) {
-        const f16x8 even = operand(c[0] & 0x000f000fu, c[1] & 0x000f000fu, c[2] & 0x000f000fu, c[3] & 0x000f000fu);
-        const f16x8 odd = operand(c[0] & 0x00f000f0u, c[1] & 0x00f000f0u, c[2] & 0x00f000f0u, c[3] & 0x00f000f0u);
+        auto low = [&](int i) { return centred<4, 0>(c[i] & 0x000f000fu); };
+        auto high = [&](int i) { return centred<4, 4>(c[i] & 0x00f000f0u); };
+        const f16x8 even = operand(low(0), low(1), low(2), low(3));
+        const f16x8 odd = operand(high(0), high(1), high(2), high(3));
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           o[t][2 * byte] = mfma(even, pv[t][2 * byte * 16 / G], o[t][2 * byte]);
           o[t][2 * byte + 1] = mfma(odd, pv[t][2 * byte * 16 / G], o[t][2 * byte + 1]);
         }
       } else {
-        const f16x8 a = operand(c[0], c[1], c[2], c[3]);
+        auto mid = [&](int i) { return centred<8, 0>(c[i]); };
+        const f16x8 a = operand(mid(0), mid(1), mid(2), mid(3));
 #pragma unroll
         for (int t = 0; t < NT; ++t) o[t][byte] = mfma(a, pv[t][byte * 16 / G], o[t][byte]);
       }
@@ -355,62 +402,55 @@ struct Wave {
     top_step = fmaxf(top_step, __shfl_xor(top_step, 32));
     float ratio = 1.0f;
     if (top_step > elim) {      // the same in the whole wave
-      const int e = (int)(__float_as_uint(top_step) >> 23) - 127 + 1 - kStepTop;   // top_step 2^-e in [2^10, 2^11)
+      const int e = (int)(__float_as_uint(top_step) >> 23) - 127 + 1;   // top_step 2^-e in [1/2, 1)
       const float inv = ldexpf(1.0f, -e);
       ratio = elim > 0.0f ? inv / einv : 1.0f;   // powers of two
       einv = inv;
-      elim = ldexpf(1.0f, kStepTop + e);
+      elim = ldexpf(1.0f, e);
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float top = m[t];
+      float top = mb[t] + kPeak;
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) top = fmaxf(top, sc[t][s][r]);
+        for (int r = 0; r < 4; ++r) top = fmaxf(top, sc[t][s][r] * rf[t]);
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
-      const float alpha = __builtin_amdgcn_exp2f(m[t] - top);
-      m[t] = top;
-      l[t] *= alpha;
+      top -= kPeak;
+      const float alpha = __builtin_amdgcn_exp2f(mb[t] - top);
+      mb[t] = top;
+      st[t] *= alpha;
       const float both = alpha * ratio;
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        zc[t][g] *= alpha;
-        hs[t][g] *= both;
-      }
 #pragma unroll
       for (int i = 0; i < kTiles; ++i) o[t][i] *= both;
     }
   }
 
-  // Sums over the four lanes of a row, and the outputs in units of exp2(m): o in place.
-  __device__ __forceinline__ void finish() {
-    const float up = 0x1p24f / einv;
+  // Row `row` of the sums' result for this lane's query row, from the lane that holds it.
+  __device__ __forceinline__ float sum_of(int t, int row) const {
+    return __shfl(st[t][row % 4], (int)(threadIdx.x % 16) + 16 * (row / 4));
+  }
+
+  // The sum of probabilities of tile t's rows; the outputs in the same units, in place of o.
+  __device__ __forceinline__ float finish(int t) {
+    const float up = 0x1p9f / einv;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      l[t] += __shfl_xor(l[t], 16);
-      l[t] += __shfl_xor(l[t], 32);
+    for (int g = 0; g < kGroups; ++g) {
+      const float z = fmaf(kHalf, sum_of(t, 1 + kGroups + g), sum_of(t, 1 + g));
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        zc[t][g] += __shfl_xor(zc[t][g], 16);
-        zc[t][g] += __shfl_xor(zc[t][g], 32);
-      }
+      for (int i = g * G / 16; i < (g + 1) * G / 16; ++i)
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        const float in = BITS == 4 && (i & 1) ? 0.0625f : 1.0f;
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          o[t][i][r] = fmaf(fmaf(o[t][i][r], in, -hs[t][i * 16 / G][r]), up, zc[t][i * 16 / G]);
-      }
+        for (int r = 0; r < 4; ++r) o[t][i][r] = fmaf(o[t][i][r], up, z);
     }
+    return sum_of(t, 0);
   }
 };
 
 // Combine the four waves of a block that took turns over the keys of the same
 // rows: the first wave ends with the sums.
 template <int D, int NT, typename W>
-__device__ __forceinline__ void join_waves(W& w, int wave, float* lds) {
+__device__ __forceinline__ void join_waves(W& w, float (&l)[NT], int wave, float* lds) {
   constexpr int kRows = NT * 16, kStride = D + 4;
   const int n = threadIdx.x % 16, quad = threadIdx.x / 16 % 4;
   float* ml = lds;                            // [4][kRows][2]
@@ -418,8 +458,8 @@ __device__ __forceinline__ void join_waves(W& w, int wave, float* lds) {
 #pragma unroll
   for (int t = 0; t < NT; ++t)
     if (quad == 0) {
-      ml[(wave * kRows + t * 16 + n) * 2] = w.m[t];
-      ml[(wave * kRows + t * 16 + n) * 2 + 1] = w.l[t];
+      ml[(wave * kRows + t * 16 + n) * 2] = w.mb[t];
+      ml[(wave * kRows + t * 16 + n) * 2 + 1] = l[t];
     }
   __syncthreads();
 #pragma unroll
@@ -433,11 +473,11 @@ __device__ __forceinline__ void join_waves(W& w, int wave, float* lds) {
 #pragma unroll
     for (int v = 0; v < kWaves; ++v)
       sum = fmaf(ml[(v * kRows + t * 16 + n) * 2 + 1], __builtin_amdgcn_exp2f(mm[v] - top), sum);
-    const float f = __builtin_amdgcn_exp2f(w.m[t] - top);
+    const float f = __builtin_amdgcn_exp2f(w.mb[t] - top);
 #pragma unroll
     for (int i = 0; i < W::kTiles; ++i) w.o[t][i] *= f;
-    w.m[t] = top;
-    w.l[t] = sum;
+    w.mb[t] = top;
+    l[t] = sum;
   }
 #pragma unroll
   for (int half = 2; half >= 1; half /= 2) {
@@ -495,34 +535,45 @@ __global__ __launch_bounds__(kWaves * 64) void k_kv_attention(KvAttnArgs a) {
   const int lo_max = a.window > 0 ? p1 - a.window + 1 : 0, lo_min = a.window > 0 ? p0 - a.window + 1 : 0;
   const int32_t* table = a.b.page_table + (int64_t)b * a.b.table_stride;
 
-  W w;
-  w.begin(a, sq, hk, base, rows);
   constexpr int kStep = WR == 1 ? kWaves : 1;
   int t = split * a.plan.split_tiles + (WR == 1 ? wave : 0);
   const int t_end = min((split + 1) * a.plan.split_tiles, span.tiles);
   Tile<BITS, D, G> x, y;
+  Pages next;
+  // Two buffers, one in flight while the other is worked on.  A load past the
+  // last tile repeats it; nothing uses the copy.
+  auto fetch = [&](Tile<BITS, D, G>& into, int at) {
+    load_tile(into, a.c, next, hk, span.token(min(at, t_end - 1)));
+    next = tile_pages(a.c, table, sq.len, span.token(min(at + kStep, t_end - 1)));
+  };
+  W w;
+  auto work = [&](Tile<BITS, D, G>& from, int at) {
+    const int tb = span.token(at);
+    if (!(tb <= hi_max && (tb + kTile > lo_min || tb < a.sinks))) return;
+    const bool whole = tb + kTile - 1 <= hi_min && tb + kTile <= sq.len && from.ok == 3u &&
+                       (tb >= lo_max || tb + kTile <= a.sinks);
+    w.step(from, tb, !whole, sq.len, a.sinks);
+  };
   if (t < t_end) {
-    load_tile(x, a.c, tile_pages(a.c, table, sq.len, span.token(t)), hk, span.token(t));
-    Pages next = tile_pages(a.c, table, sq.len, span.token(min(t + kStep, t_end - 1)));
-    for (; t < t_end; t += kStep) {
-      const int tb = span.token(t);
-      if (t + kStep < t_end) {
-        load_tile(y, a.c, next, hk, span.token(t + kStep));
-        next = tile_pages(a.c, table, sq.len, span.token(min(t + 2 * kStep, t_end - 1)));
-      }
-      const bool seen = tb <= hi_max && (tb + kTile > lo_min || tb < a.sinks);
-      if (seen) {
-        const bool whole = tb + kTile - 1 <= hi_min && tb + kTile <= sq.len && x.ok == 3u &&
-                           (tb >= lo_max || tb + kTile <= a.sinks);
-        if (whole) w.template step<false>(x, tb, sq.len, a.sinks);
-        else w.template step<true>(x, tb, sq.len, a.sinks);
-      }
-      x = y;
+    next = tile_pages(a.c, table, sq.len, span.token(t));
+    fetch(x, t);
+    w.begin(a, sq, hk, base, rows);
+    for (;;) {
+      fetch(y, t + kStep);
+      work(x, t);
+      if ((t += kStep) >= t_end) break;
+      fetch(x, t + kStep);
+      work(y, t);
+      if ((t += kStep) >= t_end) break;
     }
+  } else {
+    w.begin(a, sq, hk, base, rows);
   }
-  w.finish();
+  float l[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) l[i] = w.finish(i);
   if constexpr (WR == 1) {
-    join_waves<D, NT>(w, wave, lds);
+    join_waves<D, NT>(w, l, wave, lds);
     if (wave != 0) return;
   }
   const int n = threadIdx.x % 16, quad = threadIdx.x / 16 % 4;
@@ -532,15 +583,15 @@ __global__ __launch_bounds__(kWaves * 64) void k_kv_attention(KvAttnArgs a) {
     if (row >= rows) continue;
     if (active <= 1) {
       const int i = row / a.heads_per_kv, h = hk * a.heads_per_kv + row - i * a.heads_per_kv;
-      const float inv = w.l[t2] > 0.0f ? 1.0f / w.l[t2] : w.l[t2] == 0.0f ? 0.0f : w.l[t2];   // nothing visible: 0; NaN stays
+      const float inv = l[t2] == 0.0f ? 0.0f : 1.0f / l[t2];   // a row that sees nothing becomes 0
       const int64_t e = (int64_t)(sq.first + i) * a.out.row_stride + (int64_t)h * a.out.head_stride + quad * 4;
 #pragma unroll
       for (int i2 = 0; i2 < W::kTiles; ++i2) store_out4(a.out, e + i2 * 16, w.o[t2][i2] * inv);
     } else {
       const int64_t at = part_index(a, b, hk, a.plan.row_blocks * kBlockRows, row, split);
       if (quad == 0) {
-        a.part_ml[at * 2] = w.m[t2];
-        a.part_ml[at * 2 + 1] = w.l[t2];
+        a.part_ml[at * 2] = w.mb[t2];
+        a.part_ml[at * 2 + 1] = l[t2];
       }
 #pragma unroll
       for (int i2 = 0; i2 < W::kTiles; ++i2)

@@ -39,7 +39,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_kv_join(KvAttnArgs a, int block
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = fmaf(a.part_o[(at + s) * D + lane * E + e], f, o[e]);
   }
-  const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   const int i = row / a.heads_per_kv, h = hk * a.heads_per_kv + row - i * a.heads_per_kv;
   uint16_t* out = static_cast<uint16_t*>(a.out.p) + (int64_t)(sq.first + i) * a.out.row_stride +
                   (int64_t)h * a.out.head_stride + lane * E;
