@@ -187,7 +187,11 @@ struct Wave {
   float rf[NT];                  // raw score -> log2 units
   int lo[NT], hi[NT];            // visible keys: j <= hi and (j >= lo or j < sinks)
   f32x4 o[NT][kTiles];           // sum of p step einv (c - kHalf) 2^-9
-  f32x4 st[NT];                  // rows of the 16x16 result: 0 sum p; 1 + g sum p zero; 1 + kGroups + g sum p step
+  // Rows of a 16x16 result: g: sum p zero; kGroups + g: sum p step; 2 kGroups:
+  // sum p.  Eight groups leave no row for the last, which is added up in `l`.
+  static constexpr bool kSumRow = 2 * kGroups < 16;
+  f32x4 st[NT];
+  float l[NT];                   // (!kSumRow) this lane's part of sum p
   float mb[NT];                  // running maximum (log2) - kPeak
   float einv, elim;              // einv: a power of two with step einv <= 1 while every step <= elim
   uint32_t psel, por;            // how this lane builds its row of the operand that gives `st`
@@ -259,12 +263,13 @@ struct Wave {
 #pragma unroll
       for (int i2 = 0; i2 < kTiles; ++i2) o[t][i2] = f32x4{0, 0, 0, 0};
       mb[t] = kLowest;
+      l[t] = 0.0f;
     }
     einv = 1.0f;
     elim = 0.0f;
-    psel = n >= 1 && n <= kGroups ? 0x07060302u : n > kGroups && n <= 2 * kGroups ? 0x05040100u : 0x0c0c0c0cu;
-    por = n == 0 ? 0x3c003c00u : 0u;
-    pgroup = n > kGroups ? n - kGroups - 1 : n - 1;
+    psel = n < kGroups ? 0x07060302u : n < 2 * kGroups ? 0x05040100u : 0x0c0c0c0cu;
+    por = n == 2 * kGroups ? 0x3c003c00u : 0u;
+    pgroup = n < kGroups ? n : n - kGroups;
   }
 
   // One tile of 32 keys at token tb; masked: some of them some row may not see.
@@ -336,7 +341,7 @@ struct Wave {
 #pragma unroll
           for (int r = 0; r < 4; ++r) y[t][s][r] = fmaf(sc[t][s][r], rf[t], -mb[t]);
     }
-    // the operand of the sums that need no code: row 0 ones, then zeros, then steps
+    // the operand of the sums that need no code: zeros, steps, ones
     uint32_t sw[2][4];
 #pragma unroll
     for (int s = 0; s < 2; ++s)
@@ -364,6 +369,7 @@ struct Wave {
         for (int r = 0; r < 4; ++r) {
           const float e = __builtin_amdgcn_exp2f(y[t][s][r]);
           p[4 * s + r] = (_Float16)e;
+          if constexpr (!kSumRow) l[t] += e;
 #pragma unroll
           for (int g = 0; g < kGroups; ++g) pv[t][g][4 * s + r] = (_Float16)(e * vs[s][r][g]);
         }
@@ -421,6 +427,7 @@ struct Wave {
       const float alpha = __builtin_amdgcn_exp2f(mb[t] - top);
       mb[t] = top;
       st[t] *= alpha;
+      l[t] *= alpha;
       const float both = alpha * ratio;
 #pragma unroll
       for (int i = 0; i < kTiles; ++i) o[t][i] *= both;
@@ -437,13 +444,15 @@ struct Wave {
     const float up = 0x1p9f / einv;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      const float z = fmaf(kHalf, sum_of(t, 1 + kGroups + g), sum_of(t, 1 + g));
+      const float z = fmaf(kHalf, sum_of(t, kGroups + g), sum_of(t, g));
 #pragma unroll
       for (int i = g * G / 16; i < (g + 1) * G / 16; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r) o[t][i][r] = fmaf(o[t][i][r], up, z);
     }
-    return sum_of(t, 0);
+    if constexpr (kSumRow) return sum_of(t, 2 * kGroups);
+    float sum = l[t] + __shfl_xor(l[t], 16);
+    return sum + __shfl_xor(sum, 32);
   }
 };
 
