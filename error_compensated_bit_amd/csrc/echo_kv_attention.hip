@@ -54,7 +54,11 @@ __device__ __forceinline__ f16x8 operand(uint32_t a, uint32_t b, uint32_t c, uin
   return __builtin_bit_cast(f16x8, w);
 }
 
-// What one step loads: keys and values of 2 x 16 tokens and their parameters.
+// What one step loads: keys and values of 2 x 16 tokens, and their parameters
+// spread over the lanes (word 64 i + lane of [keys, values][half][token][group]).
+// Every lane needs the parameters of 8 tokens, and loading them there would take
+// 16 registers a group and buffer; they go through a few LDS words of the
+// wave's own instead.
 template <int BITS, int D, int G>
 struct Tile {
   static constexpr int kRowBytes = D * BITS / 8;
@@ -64,7 +68,8 @@ struct Tile {
   static constexpr int kGroups = D / G;
   uint32_t k[2][kKeyWords];
   uint32_t v[2][4][kUnitWords];
-  uint32_t kp[2][4][kGroups], vp[2][4][kGroups];
+  static constexpr int kParamWords = 64 * kGroups;       // of a tile
+  uint32_t param[kGroups];
   uint32_t ok;   // bit s: the 16 tokens of half s lie in a page of the cache
 };
 
@@ -109,7 +114,7 @@ __device__ __forceinline__ void load_tile(Tile<BITS, D, G>& x, const KvCache& c,
   const uint32_t n = threadIdx.x % 16, quad = threadIdx.x / 16 % 4;
   const uint32_t k_at = n * T::kRowBytes + quad * (T::kRowBytes / 4);
   const uint32_t v_at = quad * 4 * T::kRowBytes + n * T::kUnitBytes;
-  const uint32_t p_at = quad * 16 * T::kGroups;
+  const uint8_t* param[2][2];
   x.ok = 0;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
@@ -119,17 +124,31 @@ __device__ __forceinline__ void load_tile(Tile<BITS, D, G>& x, const KvCache& c,
     const int64_t row = ((page * c.kv_heads + hk) << c.page_shift) + ((tb + 16 * s) & ((1 << c.page_shift) - 1));
     const uint8_t* kc = c.k_codes + row * T::kRowBytes;
     const uint8_t* vc = c.v_codes + row * T::kRowBytes;
-    const uint8_t* kp = reinterpret_cast<const uint8_t*>(c.k_params) + row * (4 * T::kGroups);
-    const uint8_t* vp = reinterpret_cast<const uint8_t*>(c.v_params) + row * (4 * T::kGroups);
+    param[0][s] = reinterpret_cast<const uint8_t*>(c.k_params + row * T::kGroups);
+    param[1][s] = reinterpret_cast<const uint8_t*>(c.v_params + row * T::kGroups);
     load_words<T::kKeyWords>(kc + k_at, x.k[s]);
-    load_words<4 * T::kGroups>(kp + p_at, &x.kp[s][0][0]);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       if constexpr (T::kUnitBytes == 2) x.v[s][r][0] = *reinterpret_cast<const uint16_t*>(vc + v_at + r * T::kRowBytes);
       else load_words<T::kUnitWords>(vc + v_at + r * T::kRowBytes, x.v[s][r]);
     }
-    load_words<4 * T::kGroups>(vp + p_at, &x.vp[s][0][0]);
   }
+#pragma unroll
+  for (int i = 0; i < T::kGroups; ++i) {
+    const uint32_t w = i * 64 + threadIdx.x % 64;
+    const uint32_t run = w / (16 * T::kGroups);          // 0, 1: keys of each half; 2, 3: values
+    const uint8_t* lo = run & 1 ? param[0][1] : param[0][0];
+    const uint8_t* hi = run & 1 ? param[1][1] : param[1][0];
+    const uint8_t* p = run & 2 ? hi : lo;
+    x.param[i] = *reinterpret_cast<const uint32_t*>(p + w % (16 * T::kGroups) * 4);
+  }
+}
+
+// LDS written by other lanes of this wave is visible behind this.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // Codes of slice w (32 elements) of a lane's share of a key row, as the halves
@@ -177,19 +196,108 @@ __device__ __forceinline__ void store_out4(const KvRows& out, int64_t e, f32x4 v
   *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out.p) + e) = w;
 }
 
+// The operand of value tile i (elements 16 i + 0..15) from a lane's shares of 8 tokens.
+template <int BITS, int WORDS>
+__device__ __forceinline__ f16x8 value_operand(const uint32_t (&v)[2][4][WORDS], int i) {
+  const int byte = i * BITS / 8;
+  auto half = [&](int s, int r) {
+    const uint32_t c = byte_pair(v[s][r], v[s][r + 1], byte);
+    if constexpr (BITS == 8) return centred<8, 0>(c);
+    else return i & 1 ? centred<4, 4>(c & 0x00f000f0u) : centred<4, 0>(c & 0x000f000fu);
+  };
+  return operand(half(0, 0), half(0, 2), half(1, 0), half(1, 2));
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+// op over aligned runs of LANES = 4 .. 32 lanes, the result in every lane of the run.
+template <int LANES, typename Op>
+__device__ __forceinline__ float run_reduce(float v, Op op) {
+  v = op(v, dpp<0xB1>(v));                            // quad_perm [1,0,3,2]
+  v = op(v, dpp<0x4E>(v));                            // quad_perm [2,3,0,1]
+  if constexpr (LANES >= 8) v = op(v, dpp<0x141>(v));   // lane i <-> 7-i within 8
+  if constexpr (LANES >= 16) v = op(v, dpp<0x140>(v));  // lane i <-> 15-i within 16
+  if constexpr (LANES >= 32)
+    v = op(v, __builtin_bit_cast(float, __builtin_amdgcn_ds_swizzle(__builtin_bit_cast(int, v), 0x401F)));
+  return v;
+}
+
+// Query rows of a block in LDS: their matrix operands, and what turns a raw
+// score into log2 units.
+template <int BITS, int D, int G, int ROWS>
+struct QueryRows {
+  static constexpr int kSlices = D / 32, kGroups = D / G, kRuns = D / 8;
+  f16x8 op[ROWS / 16][kSlices][64];
+  float rf[ROWS], qs[ROWS][kGroups];
+
+  // Rows row0 .. row0 + ROWS - 1 of a (sequence, K/V head) with `rows` rows; those behind the last are 0.
+  template <int THREADS>
+  __device__ __forceinline__ void stage(const KvAttnArgs& a, const Seq& sq, int hk, int row0, int rows) {
+    static_assert(ROWS * kRuns % 64 == 0, "whole waves");
+#pragma unroll
+    for (int pass = 0; pass * THREADS < ROWS * kRuns; ++pass) {
+      const int unit = pass * THREADS + threadIdx.x, r = unit / kRuns, run = unit % kRuns;
+      if (unit >= ROWS * kRuns) break;
+      const int row = row0 + r;
+      u32x4 raw = {0, 0, 0, 0};
+      if (row < rows) {
+        const int i = row / a.heads_per_kv, h = row - i * a.heads_per_kv;
+        raw = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.q.p) +
+                                              (int64_t)(sq.first + i) * a.q.row_stride +
+                                              (int64_t)(hk * a.heads_per_kv + h) * a.q.head_stride + run * 8);
+      }
+      float x[8], top = 0.0f;
+      if (a.q.dtype == kKvF16) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = f16_to_f32(j & 1 ? raw[j / 2] >> 16 : raw[j / 2] & 0xffffu);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(j & 1 ? raw[j / 2] & 0xffff0000u : raw[j / 2] << 16);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
+      top = run_reduce<kRuns>(top, [](float u, float v) { return fmaxf(u, v); });
+      // a power of two takes the row's largest element into [2^14, 2^15): bf16
+      // values keep all their bits down to 2^-24 of the largest
+      const int field = (int)(__float_as_uint(top) >> 23);
+      const int up = field == 0 || field == 255 ? 0 : 14 - (field - 127);
+      _Float16 e[8];
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        e[j] = (_Float16)ldexpf(x[j], up);
+        sum += (float)e[j];
+      }
+      sum = run_reduce<G / 8>(sum, [](float u, float v) { return u + v; });
+      f16x8 o;
+      if constexpr (BITS == 4) {
+        const _Float16 low = (_Float16)0.0625f;   // codes one nibble higher count 16 times
+        o = f16x8{e[0], e[4], e[1] * low, e[5] * low, e[2], e[6], e[3] * low, e[7] * low};
+      } else {
+        o = f16x8{e[0], e[2], e[1], e[3], e[4], e[6], e[5], e[7]};
+      }
+      op[r / 16][run / 4][run % 4 * 16 + r % 16] = o;
+      if (run == 0) rf[r] = ldexpf(a.scale_log2, 24 - up);
+      if (run % (G / 8) == 0) qs[r][run / (G / 8)] = sum * 0x1p-24f;
+    }
+  }
+};
+
 // The state of a wave: 16 NT query rows against the keys seen so far.
 template <int BITS, int D, int G, int NT>
 struct Wave {
   static constexpr int kSlices = D / 32, kTiles = D / 16, kGroups = D / G;
   static constexpr float kHalf = BITS == 4 ? 8.0f : 128.0f;
+  // Rows of `st`: g: sum p zero; kGroups + g: sum p step; 2 kGroups: sum p.
+  // Eight groups leave no row for the last, which is added up in `l`.
+  static constexpr bool kSumRow = 2 * kGroups < 16;
   f16x8 q[NT][kSlices];          // query rows as matrix operands, scaled to [2^14, 2^15)
   float qs[NT][kGroups];         // sum of a row's q over a group, * 2^-24
   float rf[NT];                  // raw score -> log2 units
   int lo[NT], hi[NT];            // visible keys: j <= hi and (j >= lo or j < sinks)
   f32x4 o[NT][kTiles];           // sum of p step einv (c - kHalf) 2^-9
-  // Rows of a 16x16 result: g: sum p zero; kGroups + g: sum p step; 2 kGroups:
-  // sum p.  Eight groups leave no row for the last, which is added up in `l`.
-  static constexpr bool kSumRow = 2 * kGroups < 16;
   f32x4 st[NT];
   float l[NT];                   // (!kSumRow) this lane's part of sum p
   float mb[NT];                  // running maximum (log2) - kPeak
@@ -197,71 +305,26 @@ struct Wave {
   uint32_t psel, por;            // how this lane builds its row of the operand that gives `st`
   int pgroup;
 
-  // The rows base .. base + 16 NT - 1 of a (sequence, K/V head) with `rows` rows.
-  __device__ __forceinline__ void begin(const KvAttnArgs& a, const Seq& sq, int hk, int base, int rows) {
-    const int n = threadIdx.x % 16, quad = threadIdx.x / 16 % 4;
+  // Rows row0 + first .. of the block's staged rows.
+  template <int ROWS>
+  __device__ __forceinline__ void begin(const KvAttnArgs& a, const Seq& sq, const QueryRows<BITS, D, G, ROWS>& from,
+                                        int row0, int first, int rows) {
+    const int n = threadIdx.x % 16, lane = threadIdx.x % 64;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int row = base + t * 16 + n;
+      const int r = first + t * 16 + n, row = row0 + r;
       const bool exists = row < rows;
-      const int i = row / a.heads_per_kv, h = row - i * a.heads_per_kv;
-      const int pos = sq.len - sq.n + i;
+      const int pos = sq.len - sq.n + row / a.heads_per_kv;
       hi[t] = !a.causal || !exists ? sq.len - 1 : pos < sq.len ? pos : sq.len - 1;
       lo[t] = a.window > 0 && exists ? (int)max((int64_t)pos - a.window + 1, (int64_t)0) : 0;
-      const uint16_t* src = static_cast<const uint16_t*>(a.q.p) + (int64_t)(sq.first + (exists ? i : 0)) * a.q.row_stride +
-                            (int64_t)(hk * a.heads_per_kv + (exists ? h : 0)) * a.q.head_stride + quad * 8;
-      u32x4 raw[kSlices];
+      rf[t] = from.rf[r];
 #pragma unroll
-      for (int w = 0; w < kSlices; ++w) raw[w] = *reinterpret_cast<const u32x4*>(src + w * 32);
-      auto value = [&](int w, int j) {
-        const uint32_t bits = j & 1 ? raw[w][j / 2] >> 16 : raw[w][j / 2] & 0xffffu;
-        return exists ? (a.q.dtype == kKvF16 ? f16_to_f32(bits) : bf16_to_f32(bits)) : 0.0f;
-      };
-      float top = 0.0f;
+      for (int g = 0; g < kGroups; ++g) qs[t][g] = from.qs[r][g];
 #pragma unroll
-      for (int w = 0; w < kSlices; ++w)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(value(w, j)));
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      // a power of two takes the row's largest element into [2^14, 2^15): bf16
-      // values keep all their bits down to 2^-24 of the largest
-      const int field = (int)(__float_as_uint(top) >> 23);
-      const int up = field == 0 || field == 255 ? 0 : 14 - (field - 127);
-      rf[t] = ldexpf(a.scale_log2, 24 - up);
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) qs[t][g] = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kSlices; ++w) {
-        _Float16 e[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float x = ldexpf(value(w, j), up);
-          e[j] = (_Float16)x;
-          qs[t][w * 32 / G] += (float)e[j];
-        }
-        f16x8 op;
-        const _Float16 low = (_Float16)0.0625f;
-        if constexpr (BITS == 4) {
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            op[2 * v] = v & 1 ? e[v] * low : e[v];
-            op[2 * v + 1] = v & 1 ? e[v + 4] * low : e[v + 4];
-          }
-        } else {
-          op = f16x8{e[0], e[2], e[1], e[3], e[4], e[6], e[5], e[7]};
-        }
-        q[t][w] = op;
-      }
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        qs[t][g] += __shfl_xor(qs[t][g], 16);
-        qs[t][g] += __shfl_xor(qs[t][g], 32);
-        qs[t][g] *= 0x1p-24f;
-      }
+      for (int w = 0; w < kSlices; ++w) q[t][w] = from.op[first / 16 + t][w][lane];
       st[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int i2 = 0; i2 < kTiles; ++i2) o[t][i2] = f32x4{0, 0, 0, 0};
+      for (int i = 0; i < kTiles; ++i) o[t][i] = f32x4{0, 0, 0, 0};
       mb[t] = kLowest;
       l[t] = 0.0f;
     }
@@ -269,15 +332,30 @@ struct Wave {
     elim = 0.0f;
     psel = n < kGroups ? 0x07060302u : n < 2 * kGroups ? 0x05040100u : 0x0c0c0c0cu;
     por = n == 2 * kGroups ? 0x3c003c00u : 0u;
-    pgroup = n < kGroups ? n : n - kGroups;
+    pgroup = n % kGroups;
   }
 
   // One tile of 32 keys at token tb; masked: some of them some row may not see.
-  __device__ __forceinline__ void step(Tile<BITS, D, G>& x, int tb, bool masked, int len, int sinks) {
+  // key(s, w): operand of slice w of half s; value(i): operand of value tile i;
+  // param: the tile's parameters in LDS, 0 where there is no key; ok: as in Tile.
+  template <typename Key, typename Value>
+  __device__ __forceinline__ void step(const uint32_t* param, Key&& key, Value&& value, int tb, bool masked, int len,
+                                       uint32_t ok, int sinks) {
     const int quad = threadIdx.x / 16 % 4;
+    // words of tokens quad * 4 + 0..3 of half s, group minor
+    auto params = [&](int array, int s, uint32_t (&w)[4][kGroups]) {
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(param + ((array * 2 + s) * 16 + quad * 4) * kGroups + 4 * i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[(4 * i + e) / kGroups][(4 * i + e) % kGroups] = v[e];
+      }
+    };
     float sc[NT][2][4];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
+      uint32_t kp[4][kGroups];
+      params(0, s, kp);
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         f32x4 acc[NT];
@@ -285,13 +363,13 @@ struct Wave {
         for (int t = 0; t < NT; ++t) acc[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int w = g * G / 32; w < (g + 1) * G / 32; ++w) {
-          const f16x8 a = key_operand<BITS>(x.k[s], w);
+          const f16x8 a = key(s, w);
 #pragma unroll
           for (int t = 0; t < NT; ++t) acc[t] = mfma(a, q[t][w], acc[t]);
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float ks = f16_to_f32(x.kp[s][r][g] & 0xffffu), kz = f16_to_f32(x.kp[s][r][g] >> 16);
+          const float ks = f16_to_f32(kp[r][g] & 0xffffu), kz = f16_to_f32(kp[r][g] >> 16);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             const float z = g == 0 ? kz * qs[t][g] : fmaf(kz, qs[t][g], sc[t][s][r]);
@@ -306,24 +384,23 @@ struct Wave {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int j = tb + 16 * s + quad * 4 + r;
-          const bool there = j < len && (x.ok >> s & 1u);
-#pragma unroll
-          for (int g = 0; g < kGroups; ++g)
-            if (!there) x.vp[s][r][g] = 0u;   // slots behind the last key hold anything
+          const bool there = j < len && (ok >> s & 1u);
 #pragma unroll
           for (int t = 0; t < NT; ++t)
             if (!(there && j <= hi[t] && (j >= lo[t] || j < sinks))) sc[t][s][r] = rf[t] < 0.0f ? INFINITY : -INFINITY;
         }
     }
     float y[NT][2][4], vs[2][4][kGroups];
+    uint32_t vp[2][4][kGroups];
     float top_y = -INFINITY, top_step = 0.0f;
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int s = 0; s < 2; ++s) {
+      params(1, s, vp[s]);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-          vs[s][r][g] = f16_to_f32(x.vp[s][r][g] & 0xffffu);
+          vs[s][r][g] = f16_to_f32(vp[s][r][g] & 0xffffu);
           top_step = fmaxf(top_step, vs[s][r][g]);
         }
 #pragma unroll
@@ -332,6 +409,7 @@ struct Wave {
           top_y = fmaxf(top_y, y[t][s][r]);
         }
       }
+    }
     if (__any(top_y > kPeak + kSlack || top_step > elim)) {
       rescale(sc, top_step);
 #pragma unroll
@@ -347,9 +425,8 @@ struct Wave {
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        sw[s][r] = x.vp[s][r][0];
-#pragma unroll
-        for (int g = 1; g < kGroups; ++g) sw[s][r] = pgroup == g ? x.vp[s][r][g] : sw[s][r];
+        if constexpr (kGroups == 1) sw[s][r] = vp[s][r][0];
+        else sw[s][r] = param[((2 + s) * 16 + quad * 4 + r) * kGroups + pgroup];
       }
     auto pick = [&](int s, int r) { return __builtin_amdgcn_perm(sw[s][r + 1], sw[s][r], psel) | por; };
     const f16x8 sums = operand(pick(0, 0), pick(0, 2), pick(1, 0), pick(1, 2));
@@ -376,29 +453,10 @@ struct Wave {
       st[t] = mfma(sums, p, st[t]);
     }
 #pragma unroll
-    for (int byte = 0; byte < kTiles * BITS / 8; ++byte) {
-      uint32_t c[4];
+    for (int i = 0; i < kTiles; ++i) {
+      const f16x8 a = value(i);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        c[2 * s] = byte_pair(x.v[s][0], x.v[s][1], byte);
-        c[2 * s + 1] = byte_pair(x.v[s][2], x.v[s][3], byte);
-      }
-      if constexpr (BITS == 4) {
-        auto low = [&](int i) { return centred<4, 0>(c[i] & 0x000f000fu); };
-        auto high = [&](int i) { return centred<4, 4>(c[i] & 0x00f000f0u); };
-        const f16x8 even = operand(low(0), low(1), low(2), low(3));
-        const f16x8 odd = operand(high(0), high(1), high(2), high(3));
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          o[t][2 * byte] = mfma(even, pv[t][2 * byte * 16 / G], o[t][2 * byte]);
-          o[t][2 * byte + 1] = mfma(odd, pv[t][2 * byte * 16 / G], o[t][2 * byte + 1]);
-        }
-      } else {
-        auto mid = [&](int i) { return centred<8, 0>(c[i]); };
-        const f16x8 a = operand(mid(0), mid(1), mid(2), mid(3));
-#pragma unroll
-        for (int t = 0; t < NT; ++t) o[t][byte] = mfma(a, pv[t][byte * 16 / G], o[t][byte]);
-      }
+      for (int t = 0; t < NT; ++t) o[t][i] = mfma(a, pv[t][i * 16 / G], o[t][i]);
     }
   }
 
@@ -456,155 +514,334 @@ struct Wave {
   }
 };
 
-// Combine the four waves of a block that took turns over the keys of the same
-// rows: the first wave ends with the sums.
-template <int D, int NT, typename W>
-__device__ __forceinline__ void join_waves(W& w, float (&l)[NT], int wave, float* lds) {
-  constexpr int kRows = NT * 16, kStride = D + 4;
-  const int n = threadIdx.x % 16, quad = threadIdx.x / 16 % 4;
-  float* ml = lds;                            // [4][kRows][2]
-  float* part = lds + kWaves * kRows * 2;     // [2][kRows][kStride]
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-    if (quad == 0) {
-      ml[(wave * kRows + t * 16 + n) * 2] = w.mb[t];
-      ml[(wave * kRows + t * 16 + n) * 2 + 1] = l[t];
-    }
-  __syncthreads();
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    float mm[kWaves], top = kLowest, sum = 0.0f;
-#pragma unroll
-    for (int v = 0; v < kWaves; ++v) {
-      mm[v] = ml[(v * kRows + t * 16 + n) * 2];
-      top = fmaxf(top, mm[v]);
-    }
-#pragma unroll
-    for (int v = 0; v < kWaves; ++v)
-      sum = fmaf(ml[(v * kRows + t * 16 + n) * 2 + 1], __builtin_amdgcn_exp2f(mm[v] - top), sum);
-    const float f = __builtin_amdgcn_exp2f(w.mb[t] - top);
-#pragma unroll
-    for (int i = 0; i < W::kTiles; ++i) w.o[t][i] *= f;
-    w.mb[t] = top;
-    l[t] = sum;
-  }
-#pragma unroll
-  for (int half = 2; half >= 1; half /= 2) {
-    if (wave >= half && wave < 2 * half) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < W::kTiles; ++i)
-          *reinterpret_cast<f32x4*>(part + ((wave - half) * kRows + t * 16 + n) * kStride + i * 16 + quad * 4) = w.o[t][i];
-    }
-    __syncthreads();
-    if (wave < half) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < W::kTiles; ++i)
-          w.o[t][i] += *reinterpret_cast<const f32x4*>(part + (wave * kRows + t * 16 + n) * kStride + i * 16 + quad * 4);
-    }
-    __syncthreads();
-  }
-}
-
-template <int D, int NT>
-constexpr int join_floats() {
-  return kWaves * NT * 16 * 2 + 2 * NT * 16 * (D + 4);
-}
+// What a block works on, and the bounds over a range of its rows: a tile inside
+// all of them needs no mask, one outside all of them nothing.
+struct Block {
+  Seq sq;
+  Span span;
+  int b, hk, split, row0, rows, active, t0, t1;
+  const int32_t* table;
+};
+struct Bounds {
+  int hi_min, hi_max, lo_min, lo_max;
+};
 
 // grid.x: K/V head fastest, then split, then block of rows (the last rows
 // first: under a causal mask they have the most keys); grid.y: sequence.
-template <int BITS, int D, int G, int NT, int WR>
-__global__ __launch_bounds__(kWaves * 64) void k_kv_attention(KvAttnArgs a) {
-  using W = Wave<BITS, D, G, NT>;
-  constexpr int kBlockRows = NT * 16 * WR;
-  __shared__ float lds[WR == 1 ? join_floats<D, NT>() : 1];
-  const int b = blockIdx.y;
-  const int hk = blockIdx.x % a.c.kv_heads;
+// False: the block has nothing to do.
+__device__ __forceinline__ bool block_of(const KvAttnArgs& a, int block_rows, Block& k) {
+  k.b = blockIdx.y;
+  k.hk = blockIdx.x % a.c.kv_heads;
   const int rest = blockIdx.x / a.c.kv_heads;
-  const int split = rest % a.plan.splits;
-  const int rb = a.plan.row_blocks - 1 - rest / a.plan.splits;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const Seq sq = sequence(a, b);
-  const int rows = sq.computed * a.heads_per_kv;
-  const int row0 = rb * kBlockRows;
-  if (row0 >= rows) return;
-  const int row1 = min(row0 + kBlockRows, rows) - 1;
-  const Span span = key_span(a, sq.len, sq.n, row0 / a.heads_per_kv, row1 / a.heads_per_kv);
-  const int active = (span.tiles + a.plan.split_tiles - 1) / a.plan.split_tiles;
-  if (split > 0 && split >= active) return;
-  const int base = row0 + (WR == 1 ? 0 : wave * NT * 16);
-  if (WR != 1 && base >= rows) return;
-  const int last = min(base + NT * 16, rows) - 1;
-  // bounds over the wave's rows: a tile inside all of them needs no mask
-  const int p0 = sq.len - sq.n + base / a.heads_per_kv, p1 = sq.len - sq.n + last / a.heads_per_kv;
-  const int hi_min = a.causal ? p0 : sq.len - 1, hi_max = a.causal ? p1 : sq.len - 1;
-  const int lo_max = a.window > 0 ? p1 - a.window + 1 : 0, lo_min = a.window > 0 ? p0 - a.window + 1 : 0;
-  const int32_t* table = a.b.page_table + (int64_t)b * a.b.table_stride;
+  k.split = rest % a.plan.splits;
+  k.sq = sequence(a, k.b);
+  k.rows = k.sq.computed * a.heads_per_kv;
+  k.row0 = (a.plan.row_blocks - 1 - rest / a.plan.splits) * block_rows;
+  if (k.row0 >= k.rows) return false;
+  const int last = min(k.row0 + block_rows, k.rows) - 1;
+  k.span = key_span(a, k.sq.len, k.sq.n, k.row0 / a.heads_per_kv, last / a.heads_per_kv);
+  k.active = (k.span.tiles + a.plan.split_tiles - 1) / a.plan.split_tiles;
+  k.t0 = k.split * a.plan.split_tiles;
+  k.t1 = min(k.t0 + a.plan.split_tiles, k.span.tiles);
+  k.table = a.b.page_table + (int64_t)k.b * a.b.table_stride;
+  return k.split == 0 || k.split < k.active;
+}
+__device__ __forceinline__ Bounds bounds_of(const KvAttnArgs& a, const Block& k, int first, int last) {
+  const int p0 = k.sq.len - k.sq.n + first / a.heads_per_kv, p1 = k.sq.len - k.sq.n + last / a.heads_per_kv;
+  return Bounds{a.causal ? p0 : k.sq.len - 1, a.causal ? p1 : k.sq.len - 1,
+                a.window > 0 ? p0 - a.window + 1 : 0, a.window > 0 ? p1 - a.window + 1 : 0};
+}
+__device__ __forceinline__ bool tile_seen(const Bounds& r, int tb, int sinks) {
+  return tb <= r.hi_max && (tb + kTile > r.lo_min || tb < sinks);
+}
+__device__ __forceinline__ bool tile_whole(const Bounds& r, int tb, int len, uint32_t ok, int sinks) {
+  return tb + kTile - 1 <= r.hi_min && tb + kTile <= len && ok == 3u && (tb >= r.lo_max || tb + kTile <= sinks);
+}
 
-  constexpr int kStep = WR == 1 ? kWaves : 1;
-  int t = split * a.plan.split_tiles + (WR == 1 ? wave : 0);
-  const int t_end = min((split + 1) * a.plan.split_tiles, span.tiles);
-  Tile<BITS, D, G> x, y;
-  Pages next;
-  // Two buffers, one in flight while the other is worked on.  A load past the
-  // last tile repeats it; nothing uses the copy.
-  auto fetch = [&](Tile<BITS, D, G>& into, int at) {
-    load_tile(into, a.c, next, hk, span.token(min(at, t_end - 1)));
-    next = tile_pages(a.c, table, sq.len, span.token(min(at + kStep, t_end - 1)));
-  };
-  W w;
-  auto work = [&](Tile<BITS, D, G>& from, int at) {
-    const int tb = span.token(at);
-    if (!(tb <= hi_max && (tb + kTile > lo_min || tb < a.sinks))) return;
-    const bool whole = tb + kTile - 1 <= hi_min && tb + kTile <= sq.len && from.ok == 3u &&
-                       (tb >= lo_max || tb + kTile <= a.sinks);
-    w.step(from, tb, !whole, sq.len, a.sinks);
-  };
-  if (t < t_end) {
-    next = tile_pages(a.c, table, sq.len, span.token(t));
-    fetch(x, t);
-    w.begin(a, sq, hk, base, rows);
-    for (;;) {
-      fetch(y, t + kStep);
-      work(x, t);
-      if ((t += kStep) >= t_end) break;
-      fetch(x, t + kStep);
-      work(y, t);
-      if ((t += kStep) >= t_end) break;
-    }
-  } else {
-    w.begin(a, sq, hk, base, rows);
-  }
-  float l[NT];
+// A word of the tile's parameters, 0 for a token that is not there (its slot may hold anything).
+template <int GROUPS>
+__device__ __forceinline__ uint32_t there_or_zero(uint32_t word, int w, int tb, int len, uint32_t ok) {
+  const int s = w / (16 * GROUPS) & 1, j = tb + 16 * s + w % (16 * GROUPS) / GROUPS;
+  return j < len && (ok >> s & 1u) ? word : 0u;
+}
+
+__device__ __forceinline__ void store_out8(const KvRows& out, int64_t e, const float* v) {
+  u32x4 w;
+  if (out.dtype == kKvF16) {
 #pragma unroll
-  for (int i = 0; i < NT; ++i) l[i] = w.finish(i);
-  if constexpr (WR == 1) {
-    join_waves<D, NT>(w, l, wave, lds);
-    if (wave != 0) return;
+    for (int i = 0; i < 4; ++i) w[i] = f32_to_f16(v[2 * i]) | f32_to_f16(v[2 * i + 1]) << 16;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16(v[2 * i]) | f32_to_bf16(v[2 * i + 1]) << 16;
+  }
+  *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out.p) + e) = w;
+}
+
+// ------------------------------------------------------------------ few rows
+// The NW waves of a block share its 16 NT rows and take turns over the keys:
+// wave w has the tiles w, w + NW, ...  Loads go to registers, the next tile's
+// in flight during the current one's arithmetic; no barrier in the loop.  At
+// the end the waves' results meet in LDS.
+template <int BITS, int D, int G, int NT, int NW>
+struct FewLds {
+  static constexpr int kRows = NT * 16, kStride = D + 4;
+  QueryRows<BITS, D, G, kRows> q;
+  uint32_t param[NW][Tile<BITS, D, G>::kParamWords];
+  float m[NW][kRows], l[NW][kRows];
+  float o[NW][kRows][kStride];
+};
+
+// Waves per SIMD that the registers have to leave room for.
+constexpr int few_min_waves(int D, int NT) {
+  return NT == 1 ? (D == 64 ? 4 : D == 128 ? 3 : 2) : NT == 2 && D <= 128 ? 2 : 1;
+}
+
+template <int BITS, int D, int G, int NT, int NW>
+__global__ __launch_bounds__(NW * 64, few_min_waves(D, NT)) void k_kv_attention_few(KvAttnArgs a) {
+  using W = Wave<BITS, D, G, NT>;
+  using Lds = FewLds<BITS, D, G, NT, NW>;
+  extern __shared__ __align__(16) uint8_t shared[];
+  Lds& lds = *reinterpret_cast<Lds*>(shared);
+  Block k;
+  if (!block_of(a, Lds::kRows, k)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  int t = k.t0 + wave;
+  Tile<BITS, D, G> x, y;
+  Pages next = {{-1, -1}};
+  // a load past the last tile repeats it; nothing uses the copy
+  auto fetch = [&](Tile<BITS, D, G>& into, int at) {
+    load_tile(into, a.c, next, k.hk, k.span.token(min(at, k.t1 - 1)));
+    next = tile_pages(a.c, k.table, k.sq.len, k.span.token(min(at + NW, k.t1 - 1)));
+  };
+  if (t < k.t1) {
+    next = tile_pages(a.c, k.table, k.sq.len, k.span.token(t));
+    fetch(x, t);
+  }
+  lds.q.template stage<NW * 64>(a, k.sq, k.hk, k.row0, k.rows);
+  __syncthreads();
+  W w;
+  w.begin(a, k.sq, lds.q, k.row0, 0, k.rows);
+  const Bounds r = bounds_of(a, k, k.row0, min(k.row0 + Lds::kRows, k.rows) - 1);
+  uint32_t* param = lds.param[wave];
+  for (; t < k.t1; t += NW) {
+    fetch(y, t + NW);
+    const int tb = k.span.token(t);
+    if (tile_seen(r, tb, a.sinks)) {
+      const bool whole = tile_whole(r, tb, k.sq.len, x.ok, a.sinks);
+      wave_sync();
+#pragma unroll
+      for (int i = 0; i < W::kGroups; ++i) {
+        const int at = i * 64 + threadIdx.x % 64;
+        param[at] = whole ? x.param[i] : there_or_zero<W::kGroups>(x.param[i], at, tb, k.sq.len, x.ok);
+      }
+      wave_sync();
+      w.step(param, [&](int s, int i) { return key_operand<BITS>(x.k[s], i); },
+             [&](int i) { return value_operand<BITS>(x.v, i); }, tb, !whole, k.sq.len, x.ok, a.sinks);
+    }
+    x = y;
   }
   const int n = threadIdx.x % 16, quad = threadIdx.x / 16 % 4;
 #pragma unroll
-  for (int t2 = 0; t2 < NT; ++t2) {
-    const int row = base + t2 * 16 + n;
-    if (row >= rows) continue;
-    if (active <= 1) {
-      const int i = row / a.heads_per_kv, h = hk * a.heads_per_kv + row - i * a.heads_per_kv;
-      const float inv = l[t2] == 0.0f ? 0.0f : 1.0f / l[t2];   // a row that sees nothing becomes 0
-      const int64_t e = (int64_t)(sq.first + i) * a.out.row_stride + (int64_t)h * a.out.head_stride + quad * 4;
+  for (int i = 0; i < NT; ++i) {
+    const float l = w.finish(i);
+    const int row = i * 16 + n;
+    if (quad == 0) {
+      lds.m[wave][row] = w.mb[i];
+      lds.l[wave][row] = l;
+    }
 #pragma unroll
-      for (int i2 = 0; i2 < W::kTiles; ++i2) store_out4(a.out, e + i2 * 16, w.o[t2][i2] * inv);
+    for (int e = 0; e < W::kTiles; ++e) *reinterpret_cast<f32x4*>(&lds.o[wave][row][e * 16 + quad * 4]) = w.o[i][e];
+  }
+  __syncthreads();
+  constexpr int kRuns = D / 8;
+#pragma unroll
+  for (int pass = 0; pass * NW * 64 < Lds::kRows * kRuns; ++pass) {
+    const int unit = pass * NW * 64 + threadIdx.x, r0 = unit / kRuns, run = unit % kRuns;
+    const int row = k.row0 + r0;
+    if (unit >= Lds::kRows * kRuns || row >= k.rows) break;
+    float top = kLowest, sum = 0.0f, v[8] = {};
+#pragma unroll
+    for (int i = 0; i < NW; ++i) top = fmaxf(top, lds.m[i][r0]);
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const float f = __builtin_amdgcn_exp2f(lds.m[i][r0] - top);
+      sum = fmaf(lds.l[i][r0], f, sum);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = fmaf(lds.o[i][r0][run * 8 + e], f, v[e]);
+    }
+    if (k.active <= 1) {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a row that sees nothing becomes 0
+      const int i = row / a.heads_per_kv, h = k.hk * a.heads_per_kv + row - i * a.heads_per_kv;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= inv;
+      store_out8(a.out, (int64_t)(k.sq.first + i) * a.out.row_stride + (int64_t)h * a.out.head_stride + run * 8, v);
     } else {
-      const int64_t at = part_index(a, b, hk, a.plan.row_blocks * kBlockRows, row, split);
+      const int64_t at = part_index(a, k.b, k.hk, a.plan.row_blocks * Lds::kRows, row, k.split);
+      if (run == 0) {
+        a.part_ml[at * 2] = top;
+        a.part_ml[at * 2 + 1] = sum;
+      }
+      f32x4* to = reinterpret_cast<f32x4*>(a.part_o + at * D + run * 8);
+      to[0] = f32x4{v[0], v[1], v[2], v[3]};
+      to[1] = f32x4{v[4], v[5], v[6], v[7]};
+    }
+  }
+}
+
+// ------------------------------------------------------------------ many rows
+// Every wave of a block has its own 16 NT rows and all walk the same keys.  The
+// waves unpack a tile's codes once, each a quarter, into matrix operands in LDS
+// (two buffers, one barrier a tile); unpacking per wave would cost as much as
+// the softmax.  Two blocks share a compute unit, so that one's softmax runs
+// beside the other's matrix instructions without a common barrier.
+template <int BITS, int D, int G, int NT>
+struct ManyLds {
+  static constexpr int kRows = kWaves * NT * 16;
+  struct Operands {
+    f16x8 k[2][D / 32][64];
+    f16x8 v[D / 16][64];
+    uint32_t param[Tile<BITS, D, G>::kParamWords];
+  };
+  union {
+    QueryRows<BITS, D, G, kRows> q;   // before the first tile
+    Operands tile[2];
+  };
+};
+
+// A wave's quarter of a tile in registers: half s = wave / 2, part = wave % 2 of its slices and bytes.
+template <int BITS, int D, int G>
+struct Quarter {
+  using T = Tile<BITS, D, G>;
+  static constexpr int kKeyWords = T::kKeyWords / 2;          // half of a lane's share of a key row
+  static constexpr int kBytes = T::kUnitBytes / 2;            // half of its share of a value row
+  static constexpr int kWords = kBytes < 4 ? 1 : kBytes / 4;
+  static constexpr int kParams = (T::kGroups + kWaves - 1) / kWaves;
+  uint32_t k[kKeyWords], v[4][kWords], param[kParams];
+  uint32_t ok;
+
+  __device__ __forceinline__ void load(const KvCache& c, const Pages& pages, int hk, int tb, int wave) {
+    const uint32_t n = threadIdx.x % 16, quad = threadIdx.x / 16 % 4;
+    const int s = wave / 2, part = wave % 2;
+    int64_t row[2];
+    ok = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t page = pages.p[i] < 0 ? 0 : pages.p[i];   // page 0 exists; the half is masked
+      ok |= pages.p[i] < 0 ? 0u : 1u << i;
+      row[i] = ((page * c.kv_heads + hk) << c.page_shift) + ((tb + 16 * i) & ((1 << c.page_shift) - 1));
+    }
+    const int64_t mine = s ? row[1] : row[0];
+    const uint8_t* kc = c.k_codes + mine * T::kRowBytes + part * (kKeyWords * 4);
+    const uint8_t* vc = c.v_codes + mine * T::kRowBytes + part * kBytes;
+    load_words<kKeyWords>(kc + n * T::kRowBytes + quad * (T::kRowBytes / 4), k);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint8_t* u = vc + (quad * 4 + r) * T::kRowBytes + n * T::kUnitBytes;
+      if constexpr (kBytes == 1) v[r][0] = *u;
+      else if constexpr (kBytes == 2) v[r][0] = *reinterpret_cast<const uint16_t*>(u);
+      else load_words<kWords>(u, v[r]);
+    }
+#pragma unroll
+    for (int i = 0; i < kParams; ++i) {
+      const uint32_t w = (i * kWaves + wave) * 64 + threadIdx.x % 64;
+      if (T::kGroups % kWaves && w >= T::kParamWords) continue;
+      const uint32_t run = w / (16 * T::kGroups);
+      const uint32_t* from = run & 2 ? c.v_params : c.k_params;
+      param[i] = from[(run & 1 ? row[1] : row[0]) * T::kGroups + w % (16 * T::kGroups)];
+    }
+  }
+
+  template <typename Operands>
+  __device__ __forceinline__ void unpack(Operands& to, int tb, int len, int wave) const {
+    const int lane = threadIdx.x % 64, s = wave / 2, part = wave % 2;
+    constexpr int kSlices = D / 32 / 2;
+#pragma unroll
+    for (int w = 0; w < kSlices; ++w) to.k[s][part * kSlices + w][lane] = key_operand<BITS>(k, w);
+    constexpr int kTiles = D / 16 / 2;
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+      const int byte = i * BITS / 8;
+      u32x2 h;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const uint32_t c = byte_pair(v[2 * p], v[2 * p + 1], byte);
+        if constexpr (BITS == 8) h[p] = centred<8, 0>(c);
+        else h[p] = i & 1 ? centred<4, 4>(c & 0x00f000f0u) : centred<4, 0>(c & 0x000f000fu);
+      }
+      reinterpret_cast<u32x2*>(&to.v[part * kTiles + i][lane])[s] = h;
+    }
+#pragma unroll
+    for (int i = 0; i < kParams; ++i) {
+      const uint32_t w = (i * kWaves + wave) * 64 + lane;
+      if (T::kGroups % kWaves && w >= T::kParamWords) continue;
+      to.param[w] = there_or_zero<T::kGroups>(param[i], w, tb, len, ok);
+    }
+  }
+};
+
+template <int BITS, int D, int G, int NT>
+__global__ __launch_bounds__(kWaves * 64, 2) void k_kv_attention_many(KvAttnArgs a) {
+  using W = Wave<BITS, D, G, NT>;
+  using Lds = ManyLds<BITS, D, G, NT>;
+  extern __shared__ __align__(16) uint8_t shared[];
+  Lds& lds = *reinterpret_cast<Lds*>(shared);
+  Block k;
+  if (!block_of(a, Lds::kRows, k)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int first = wave * NT * 16;
+  lds.q.template stage<kWaves * 64>(a, k.sq, k.hk, k.row0, k.rows);
+  __syncthreads();
+  W w;
+  w.begin(a, k.sq, lds.q, k.row0, first, k.rows);
+  __syncthreads();   // the tiles overwrite the staged rows
+  // a wave without rows works along on those of the block's last row
+  const Bounds r = bounds_of(a, k, min(k.row0 + first, k.rows - 1), min(k.row0 + first + NT * 16, k.rows) - 1);
+  const bool idle = k.row0 + first >= k.rows;
+
+  Quarter<BITS, D, G> x;
+  uint32_t ok_now, ok_next;
+  if (k.t0 < k.t1) {
+    auto token = [&](int t) { return k.span.token(min(t, k.t1 - 1)); };   // past the last tile: that one again
+    auto fetch = [&](int t) { x.load(a.c, tile_pages(a.c, k.table, k.sq.len, token(t)), k.hk, token(t), wave); };
+    fetch(k.t0);
+    x.unpack(lds.tile[0], token(k.t0), k.sq.len, wave);
+    ok_now = x.ok;
+    fetch(k.t0 + 1);
+    __syncthreads();
+    for (int t = k.t0; t < k.t1; ++t) {
+      auto& now = lds.tile[(t - k.t0) & 1];
+      auto& then = lds.tile[(t - k.t0 + 1) & 1];
+      const int tb = k.span.token(t), lane = threadIdx.x % 64;
+      if (!idle && tile_seen(r, tb, a.sinks))
+        w.step(now.param, [&](int s, int i) { return now.k[s][i][lane]; }, [&](int i) { return now.v[i][lane]; }, tb,
+               !tile_whole(r, tb, k.sq.len, ok_now, a.sinks), k.sq.len, ok_now, a.sinks);
+      x.unpack(then, token(t + 1), k.sq.len, wave);
+      ok_next = x.ok;
+      fetch(t + 2);
+      ok_now = ok_next;
+      __syncthreads();
+    }
+  }
+  const int n = threadIdx.x % 16, quad = threadIdx.x / 16 % 4;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const float l = w.finish(i);
+    const int row = k.row0 + first + i * 16 + n;
+    if (row >= k.rows) continue;
+    if (k.active <= 1) {
+      const int tok = row / a.heads_per_kv, h = k.hk * a.heads_per_kv + row - tok * a.heads_per_kv;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const int64_t e = (int64_t)(k.sq.first + tok) * a.out.row_stride + (int64_t)h * a.out.head_stride + quad * 4;
+#pragma unroll
+      for (int d = 0; d < W::kTiles; ++d) store_out4(a.out, e + d * 16, w.o[i][d] * inv);
+    } else {
+      const int64_t at = part_index(a, k.b, k.hk, a.plan.row_blocks * Lds::kRows, row, k.split);
       if (quad == 0) {
-        a.part_ml[at * 2] = w.mb[t2];
-        a.part_ml[at * 2 + 1] = l[t2];
+        a.part_ml[at * 2] = w.mb[i];
+        a.part_ml[at * 2 + 1] = l;
       }
 #pragma unroll
-      for (int i2 = 0; i2 < W::kTiles; ++i2)
-        *reinterpret_cast<f32x4*>(a.part_o + at * D + i2 * 16 + quad * 4) = w.o[t2][i2];
+      for (int d = 0; d < W::kTiles; ++d) *reinterpret_cast<f32x4*>(a.part_o + at * D + d * 16 + quad * 4) = w.o[i][d];
     }
   }
 }
@@ -613,24 +850,42 @@ __global__ __launch_bounds__(kWaves * 64) void k_kv_attention(KvAttnArgs a) {
 
 namespace {
 
-template <int BITS, int D, int G, int NT, int WR>
-hipError_t launch_attention(const KvAttnArgs& a, hipStream_t st) {
+template <int V>
+using IC = std::integral_constant<int, V>;
+
+template <typename Lds>
+hipError_t launch_attention(void (*kernel)(KvAttnArgs), int waves, const KvAttnArgs& a, hipStream_t st) {
   const unsigned blocks = (unsigned)((int64_t)a.c.kv_heads * a.plan.row_blocks * a.plan.splits);
-  return kv_launch(kv::k_kv_attention<BITS, D, G, NT, WR>, dim3(blocks, a.b.seqs), dim3(kv::kWaves * 64), st, a);
+  static_assert(sizeof(Lds) <= 160 * 1024, "LDS of a compute unit");
+  if (sizeof(Lds) > 64 * 1024) {   // more than a launch gives without asking
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Lds));
+    if (e != hipSuccess) return e;
+  }
+  KvAttnArgs args = a;
+  void* ptrs[] = {&args};
+  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(blocks, a.b.seqs), dim3(waves * 64), ptrs,
+                         sizeof(Lds), st);
 }
 
+// Every (row_tiles, waves) that the plan gives.
 template <int BITS, int D, int G>
 hipError_t with_plan(const KvAttnArgs& a, hipStream_t st) {
   const KvPlan& p = a.plan;
+  auto few = [&](auto NT, auto NW) {
+    return launch_attention<kv::FewLds<BITS, D, G, NT(), NW()>>(kv::k_kv_attention_few<BITS, D, G, NT(), NW()>, NW(), a, st);
+  };
   if (p.row_waves == 1) {
-    if (p.row_tiles == 1) return launch_attention<BITS, D, G, 1, 1>(a, st);
-    if (p.row_tiles == 2) return launch_attention<BITS, D, G, 2, 1>(a, st);
-    if constexpr (D <= 128) return launch_attention<BITS, D, G, 4, 1>(a, st);
-  } else {
-    if (p.row_tiles == 2) return launch_attention<BITS, D, G, 2, 4>(a, st);
-    if constexpr (D <= 128) return launch_attention<BITS, D, G, 4, 4>(a, st);
+    if (p.row_tiles == 1 && p.key_waves == 4) return few(IC<1>{}, IC<4>{});
+    if (p.row_tiles == 1) return few(IC<1>{}, IC<8>{});
+    if (p.row_tiles == 2) return few(IC<2>{}, IC<4>{});
+    if constexpr (D <= 128) {
+      if (p.row_tiles == 3) return few(IC<3>{}, IC<4>{});
+    }
+    return hipErrorInvalidValue;
   }
-  return hipErrorInvalidValue;   // the plan gives no other form
+  constexpr int NT = kv_many_tiles(D);
+  return launch_attention<kv::ManyLds<BITS, D, G, NT>>(kv::k_kv_attention_many<BITS, D, G, NT>, kv::kWaves, a, st);
 }
 
 }  // namespace

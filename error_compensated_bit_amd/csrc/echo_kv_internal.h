@@ -46,6 +46,7 @@ struct KvWriteArgs {
 struct KvPlan {
   int32_t row_tiles;      // 16-row tiles a wave works on
   int32_t row_waves;      // 1: a block's waves share its rows and take turns over the keys; 4: each has its own rows
+  int32_t key_waves;      // waves of a block that share rows: 4 or 8
   int32_t row_blocks;     // blocks over the rows of one (sequence, K/V head)
   int32_t splits;         // blocks over the keys
   int32_t split_tiles;    // 32-key tiles of one split
@@ -71,6 +72,8 @@ hipError_t run_kv_attention(const KvAttnArgs& a, hipStream_t st);
 template <int BITS, int D>
 hipError_t run_kv_attention_form(const KvAttnArgs& a, hipStream_t st);
 
+// 16-row tiles of a wave where each wave has its own rows: what 256 registers hold.
+constexpr int kv_many_tiles(int head_dim) { return head_dim == 256 ? 1 : 2; }
 KvPlan kv_attention_plan(const KvCache& c, const KvBatch& b, int heads_per_kv, int causal, int window, int sinks);
 // Rows of one (sequence, K/V head) in the partial results.
 int64_t kv_plan_rows(const KvPlan& p);

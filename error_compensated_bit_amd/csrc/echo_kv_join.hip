@@ -57,13 +57,14 @@ int64_t kv_plan_rows(const KvPlan& p) { return (int64_t)p.row_blocks * plan_bloc
 KvPlan kv_attention_plan(const KvCache& c, const KvBatch& b, int heads_per_kv, int causal, int window, int sinks) {
   KvPlan p;
   const int64_t rows = (int64_t)b.max_new * heads_per_kv;
-  const int most = c.head_dim == 256 ? 2 : 4;   // tiles a wave's registers hold
+  const int most = c.head_dim == 256 ? 2 : 3;   // tiles of rows that several waves share
+  p.key_waves = 4;
   if (rows <= 16 * most) {
     p.row_waves = 1;
-    p.row_tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    p.row_tiles = (int32_t)((rows + 15) / 16);
   } else {
     p.row_waves = 4;
-    p.row_tiles = rows <= 128 ? 2 : most;
+    p.row_tiles = kv_many_tiles(c.head_dim);
   }
   const int64_t block_rows = plan_block_rows(p);
   p.row_blocks = (int32_t)((rows + block_rows - 1) / block_rows);
@@ -74,13 +75,14 @@ KvPlan kv_attention_plan(const KvCache& c, const KvBatch& b, int heads_per_kv, i
   }
   const int64_t tiles = (span + 31) / 32 > 0 ? (span + 31) / 32 : 1;
   const int64_t blocks = (int64_t)b.seqs * c.kv_heads * p.row_blocks;
-  const int64_t target = 1024;
+  const int64_t target = 512, capt = 512, lst = 8;
   int64_t splits = target / blocks;
-  const int64_t least = p.row_waves == 1 ? 8 : 16;
+  const int64_t least = p.row_waves == 1 ? lst : 16;
   if (splits > tiles / least) splits = tiles / least;
   if (splits < 1) splits = 1;
   int64_t per = (tiles + splits - 1) / splits;
-  if (p.row_waves == 1 && per > 128) per = 128;
+  if (p.row_waves == 1 && per > capt) per = capt;
+  if (p.row_waves == 1 && p.row_tiles == 1 && blocks * splits <= 256) p.key_waves = 8;
   p.split_tiles = (int32_t)per;
   p.splits = (int32_t)((tiles + per - 1) / per);
   return p;
