@@ -6,8 +6,8 @@
 // A lane has 8 consecutive elements (one 16-byte access), a row is an aligned
 // run of D/8 lanes, and a group's minimum and maximum are a butterfly of DPP
 // moves inside that run.  The order of the codes in a row is the attention
-// kernel's (echo_kv_device.h): for keys that is a permutation of the lanes'
-// words; for values the lanes exchange their codes through LDS.
+// kernel's (echo_kv_device.h): for keys a permutation of the lanes' words, for
+// values a transposition of codes between lanes, three exchanges by DPP.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -45,22 +45,24 @@ __device__ __forceinline__ void run_minmax(float& mn, float& mx) {
 }
 
 template <int DT>
-__device__ __forceinline__ void load8(const void* p, int64_t e, float* v) {
-  if constexpr (DT == kKvF32) {
-    const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + e);
-    const f32x4 a = __builtin_nontemporal_load(q), b = __builtin_nontemporal_load(q + 1);
+__device__ __forceinline__ void load8(const void* p, int64_t e, u32x4 (&w)[DT == kKvF32 ? 2 : 1]) {
+  const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(p) + e * (DT == kKvF32 ? 4 : 2));
+  w[0] = __builtin_nontemporal_load(q);
+  if constexpr (DT == kKvF32) w[1] = __builtin_nontemporal_load(q + 1);
+}
+template <int DT>
+__device__ __forceinline__ void widen8(const u32x4 (&w)[DT == kKvF32 ? 2 : 1], float* v) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
-  } else {
-    const u32x4 w = __builtin_nontemporal_load(
-        reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + e));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = DT == kKvF16 ? f16_to_f32(w[i] & 0xffffu) : bf16_to_f32(w[i] & 0xffffu);
-      v[2 * i + 1] = DT == kKvF16 ? f16_to_f32(w[i] >> 16) : bf16_to_f32(w[i] >> 16);
-    }
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (DT == kKvF32) v[i] = __uint_as_float(w[i / 4][i % 4]);
+    else if constexpr (DT == kKvF16) v[i] = f16_to_f32(i & 1 ? w[0][i / 2] >> 16 : w[0][i / 2] & 0xffffu);
+    else v[i] = (float)__builtin_bit_cast(__bf16, (uint16_t)(i & 1 ? w[0][i / 2] >> 16 : w[0][i / 2] & 0xffffu));
   }
 }
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 template <int DT>
 __device__ __forceinline__ void store8(void* p, int64_t e, const float* v) {
@@ -72,151 +74,316 @@ __device__ __forceinline__ void store8(void* p, int64_t e, const float* v) {
   } else {
     u32x4 w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = DT == kKvF16 ? f32_to_f16(v[2 * i]) | (f32_to_f16(v[2 * i + 1]) << 16)
-                          : f32_to_bf16(v[2 * i]) | (f32_to_bf16(v[2 * i + 1]) << 16);
+    for (int i = 0; i < 4; ++i) {
+      const f32x2 two = {v[2 * i], v[2 * i + 1]};
+      if constexpr (DT == kKvF16) w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(two, f16x2));
+      else w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(two, bf16x2));
+    }
     __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + e));
   }
 }
 
-// Where a lane's 8 consecutive elements are and which slot they belong to.
-// Rows are numbered token-major (token t, head h -> t * kv_heads + h).
-template <int D>
-struct Lane {
-  static constexpr int kLanes = D / 8;                  // lanes per row
-  static constexpr int kRows = kThreads / kLanes;       // rows per block
-  int t, h, run;    // run: which 8 elements
-};
-
-template <int D>
-__device__ __forceinline__ Lane<D> lane_of(int kv_heads) {
-  Lane<D> l;
-  l.run = threadIdx.x % Lane<D>::kLanes;
-  const uint32_t row = blockIdx.x * (uint32_t)Lane<D>::kRows + threadIdx.x / Lane<D>::kLanes;   // below 2^31
-  l.t = (int)(row / (uint32_t)kv_heads);
-  l.h = (int)(row - (uint32_t)l.t * (uint32_t)kv_heads);
-  return l;
+// Group parameters (see group_params): the same results without the compiler's
+// full divisions, which cost a fifth of the kernel's instructions.  span / qmax
+// is the product with the rounded reciprocal and one correction, which rounds
+// correctly wherever the quotient does not vanish in fp16 (below 2^-25 it is 0
+// either way); spans beyond 65504 qmax give 65504.  1 / step is the hardware's
+// reciprocal and one correction; it is right for every fp16 step.
+template <int BITS>
+__device__ __forceinline__ QParams group_params_fast(float mn, float mx) {
+  constexpr float qmax = (float)((1 << BITS) - 1);
+  constexpr float rq = 1.0f / qmax;
+  const float zc = fminf(fmaxf(mn, -65504.0f), 65504.0f);
+  uint32_t zb = f32_to_f16(zc);
+  zb = (zb == 0x8000u) ? 0u : zb;
+  const float zf = f16_to_f32(zb);
+  float span = mx - zf;
+  span = span > 0.0f ? fminf(span, 65504.0f * qmax) : 0.0f;
+  const float s0 = span * rq;
+  const float s = fminf(fmaf(fmaf(-qmax, s0, span), rq, s0), 65504.0f);
+  const uint32_t sb = f32_to_f16(s);
+  const float sf = f16_to_f32(sb);
+  const float y = __builtin_amdgcn_rcpf(sf);
+  const float inv = sb ? fmaf(fmaf(-sf, y, 1.0f), y, y) : 0.0f;
+  return QParams{zf, sf, inv, sb | (zb << 16)};
 }
 
-// Sequence of this lane's token: found for the wave's first and last token
-// together, and between the two by bisection.
-template <int D>
-__device__ __forceinline__ int lane_seq(const KvBatch& b, const Lane<D>& l) {
-  const int t0 = __builtin_amdgcn_readfirstlane(l.t);
-  const int t1 = __builtin_amdgcn_readlane(l.t, 63);
-  int lo = seq_of_row(b.row_start, b.seqs, t0);
-  if (t0 == t1) return lo;
-  int hi = seq_of_row(b.row_start, b.seqs, t1);
-  if (lo < 0) lo = 0;
-  while (lo < hi) {
-    const int mid = lo + (hi - lo + 1) / 2;
-    if (b.row_start[mid] <= l.t) lo = mid;
-    else hi = mid - 1;
+// Codes of 8 elements: w[0] of 8 nibbles, or w[0], w[1] of 4 bytes, in order.
+template <int BITS>
+__device__ __forceinline__ void encode8(const float* x, const QParams& q, uint32_t* w) {
+  constexpr float qmax = (float)((1 << BITS) - 1);
+  uint32_t b[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float t = __builtin_amdgcn_fmed3f((x[i] - q.zf) * q.inv, 0.0f, qmax);   // NaN: 0
+    b[i / 4] = __builtin_amdgcn_cvt_pk_u8_f32(rintf(t), i % 4, b[i / 4]);
   }
-  return lo;
+  if constexpr (BITS == 8) {
+    w[0] = b[0];
+    w[1] = b[1];
+  } else {
+    w[0] = __builtin_amdgcn_perm(b[1] | b[1] >> 4, b[0] | b[0] >> 4, 0x06040200u);
+  }
 }
 
-// Element of position c in a stored row of values.
-template <int D>
-__device__ __forceinline__ int value_element(int c) {
-  constexpr int kUnit = D / 16;
-  return (c % kUnit) * 16 + c / kUnit;
+template <int BITS>
+__device__ __forceinline__ void decode8(const uint32_t* w, uint32_t word, float* x) {
+  const float sf = f16_to_f32(word & 0xffffu), zf = f16_to_f32(word >> 16);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t c;
+    if constexpr (BITS == 8) c = w[i / 4] >> (8 * (i % 4)) & 255u;
+    else c = (i & 1 ? w[0] >> 4 & 0x0f0f0f0fu : w[0] & 0x0f0f0f0fu) >> (8 * (i / 2)) & 255u;
+    x[i] = fmaf((float)c, sf, zf);
+  }
 }
+
+// The transposition between a lane's 8 consecutive elements and the stored
+// order of values, its own inverse.  Lane r of a row has the elements 8 r + j;
+// with r = 2 i + p and the element's tile i and column m = 8 p + j, stored
+// shares run over i at fixed m.  Exchanging bit b of i (lane bit b + 1) with bit
+// b of j for b = 0, 1, 2 leaves lane (i, p) with the codes of column 8 p + i
+// (D = 128; D = 256 keeps its highest bit of i in the lane; D = 64 has two bits
+// to exchange, and j's third tells the lane's two half shares).
+template <int BIT>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t v) {   // from lane ^ 2, 4 or 8
+  if constexpr (BIT == 0) return __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true);   // quad_perm [2,3,0,1]
+  if constexpr (BIT == 1)   // xor 7, then xor 3
+    return __builtin_amdgcn_update_dpp(0, __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true), 0x1B, 0xF, 0xF, true);
+  return __builtin_amdgcn_update_dpp(0, v, 0x128, 0xF, 0xF, true);                          // row_ror:8
+}
+template <int BITS, int BIT>
+__device__ __forceinline__ void exchange_bit(uint32_t* w) {
+  const bool up = threadIdx.x >> (BIT + 1) & 1u;
+  constexpr int kDist = BITS << BIT;   // distance of the exchanged codes in bits
+  if constexpr (kDist == 32) {
+    const uint32_t got = lane_xor<BIT>(up ? w[0] : w[1]);
+    if (up) w[0] = got;
+    else w[1] = got;
+  } else {
+    constexpr uint32_t kLow = kDist == 4 ? 0x0f0f0f0fu : kDist == 8 ? 0x00ff00ffu : 0x0000ffffu;
+    const uint32_t keep = up ? ~kLow : kLow, turn = up ? kDist : 32 - kDist;
+#pragma unroll
+    for (int i = 0; i < BITS / 4; ++i) {
+      const uint32_t got = lane_xor<BIT>(w[i]);
+      w[i] = (w[i] & keep) | (__builtin_amdgcn_alignbit(got, got, turn) & ~keep);
+    }
+  }
+}
+template <int BITS, int D>
+__device__ __forceinline__ void transpose_values(uint32_t* w) {
+  exchange_bit<BITS, 0>(w);
+  exchange_bit<BITS, 1>(w);
+  if constexpr (D >= 128) exchange_bit<BITS, 2>(w);
+}
+
+// Byte offset in a stored row of values of what lane `run` holds behind the
+// transposition; D = 64: of its first half share, the second kHalf bytes on.
+template <int BITS, int D>
+__device__ __forceinline__ int value_place(int run) {
+  constexpr int kUnit = D / 16 * BITS / 8;   // bytes of a column
+  const int p = run & 1, i = run >> 1;
+  if constexpr (D == 64) return (8 * p + i) * kUnit;
+  else if constexpr (D == 128) return (8 * p + i) * kUnit;
+  else return (8 * p + i % 8) * kUnit + i / 8 * (kUnit / 2);
+}
+template <int BITS, int D>
+__device__ __forceinline__ void store_codes(uint8_t* row, int place, bool values, const uint32_t* w) {
+  if constexpr (D == 64) {
+    if (values) {
+      constexpr int kHalf = 4 * (D / 16 * BITS / 8);   // column m + 4
+      if constexpr (BITS == 4) {
+        *reinterpret_cast<uint16_t*>(row + place) = (uint16_t)w[0];
+        *reinterpret_cast<uint16_t*>(row + place + kHalf) = (uint16_t)(w[0] >> 16);
+      } else {
+        *reinterpret_cast<uint32_t*>(row + place) = w[0];
+        *reinterpret_cast<uint32_t*>(row + place + kHalf) = w[1];
+      }
+      return;
+    }
+  }
+  if constexpr (BITS == 4) *reinterpret_cast<uint32_t*>(row + place) = w[0];
+  else *reinterpret_cast<u32x2*>(row + place) = u32x2{w[0], w[1]};
+}
+template <int BITS, int D>
+__device__ __forceinline__ void load_codes(const uint8_t* row, int place, bool values, uint32_t* w) {
+  if constexpr (D == 64) {
+    if (values) {
+      constexpr int kHalf = 4 * (D / 16 * BITS / 8);
+      if constexpr (BITS == 4) {
+        w[0] = *reinterpret_cast<const uint16_t*>(row + place) |
+               (uint32_t)*reinterpret_cast<const uint16_t*>(row + place + kHalf) << 16;
+      } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(row + place);
+        w[1] = *reinterpret_cast<const uint32_t*>(row + place + kHalf);
+      }
+      return;
+    }
+  }
+  if constexpr (BITS == 4) {
+    w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(row + place));
+  } else {
+    const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(row + place));
+    w[0] = v.x;
+    w[1] = v.y;
+  }
+}
+
 // Position of the 8-element run r in a stored row of keys, in runs.
 template <int D>
 __device__ __forceinline__ int key_run(int r) {
   return (r % 4) * (D / 32) + r / 4;
 }
 
-// grid.y: 0 keys, 1 values.
-template <int BITS, int D, int G, int DT>
-__global__ __launch_bounds__(kThreads) void k_kv_write(KvCache c, KvBatch b, KvRows k, KvRows v) {
-  using L = Lane<D>;
-  __shared__ uint32_t exchange[kThreads * 2];
-  const bool values = blockIdx.y == 1;
-  const KvRows& in = values ? v : k;
-  const L l = lane_of<D>(c.kv_heads);
-  const bool exists = l.t < b.rows;
-  const int seq = lane_seq<D>(b, l);
-  RowSlot s{-1, 0};
-  if (exists) s = row_slot(c, b, seq, l.t);
-  float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (exists)
-    load8<DT>(in.p, (int64_t)l.t * in.row_stride + (int64_t)l.h * in.head_stride + l.run * 8, x);
-  float mn = x[0], mx = x[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    mn = fminf(mn, x[i]);
-    mx = fmaxf(mx, x[i]);
+constexpr int kMaxTokens = 256;   // of a block
+
+// A block's tokens t0 .. t0 + count - 1: for each, the index of its row of head
+// 0 in the cache, -1 where it has no place.  A wave looks up 64 tokens: their
+// first and last sequence together, and each lane's own between the two by
+// bisection.  Looking places up once per token and block keeps the chain of
+// dependent loads out of the rows' way.
+__device__ __forceinline__ void look_up(const KvCache& c, const KvBatch& b, int t0, int count, int64_t* place) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  if (wave * 64 >= count) return;
+  const int first = t0 + wave * 64, last = min(first + 63, t0 + count - 1);
+  const int t = min(first + (int)(threadIdx.x % 64), last);
+  int lo = seq_of_row(b.row_start, b.seqs, first);
+  int hi = first == last ? lo : seq_of_row(b.row_start, b.seqs, last);
+  if (lo < 0) lo = 0;
+  while (lo < hi) {
+    const int mid = lo + (hi - lo + 1) / 2;
+    if (b.row_start[mid] <= t) lo = mid;
+    else hi = mid - 1;
   }
-  run_minmax<G / 8>(mn, mx);
-  const QParams q = group_params<BITS>(mn, mx);
-  uint32_t code[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) code[i] = encode<BITS>(x[i], q);
-  if (values) {   // whole blocks: every lane takes part in the exchange
-    exchange[threadIdx.x * 2] = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
-    exchange[threadIdx.x * 2 + 1] = code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24;
-    __syncthreads();
-    const uint8_t* row = reinterpret_cast<const uint8_t*>(exchange) + threadIdx.x / L::kLanes * D;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) code[i] = row[value_element<D>(l.run * 8 + i)];
-  }
-  if (s.page < 0) return;
-  const int64_t r = ((s.page * c.kv_heads + l.h) << c.page_shift) + s.slot;
-  uint8_t* codes = (values ? c.v_codes : c.k_codes) + r * (D * BITS / 8);
-  const int at = values ? l.run : key_run<D>(l.run);
-  if constexpr (BITS == 4) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w |= code[i] << (4 * i);
-    reinterpret_cast<uint32_t*>(codes)[at] = w;
-  } else {
-    const u32x2 w = {code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24,
-                     code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24};
-    reinterpret_cast<u32x2*>(codes)[at] = w;
-  }
-  if (l.run % (G / 8) == 0)
-    (values ? c.v_params : c.k_params)[r * (D / G) + l.run / (G / 8)] = q.word;
+  const RowSlot s = row_slot(c, b, hi < 0 ? -1 : lo, t);
+  place[wave * 64 + threadIdx.x % 64] = s.page < 0 ? -1 : ((s.page * c.kv_heads) << c.page_shift) + s.slot;
 }
 
-template <int BITS, int D, int G, int DT>
-__global__ __launch_bounds__(kThreads) void k_kv_read(KvCache c, KvBatch b, KvRows k, KvRows v) {
-  using L = Lane<D>;
+// Rows (token, head) of a block, token-major: lane `run` of D/8 lanes has 8
+// consecutive elements of a row; a pass covers kRows rows of the block, and
+// token, head and offset move from pass to pass by additions.
+template <int D>
+struct Rows {
+  static constexpr int kLanes = D / 8;
+  static constexpr int kRows = kThreads / kLanes;
+  int t, h;            // token of the block, head
+  int64_t e;           // element offset of the lane's elements from the block's first row
+  __device__ __forceinline__ Rows(const KvRows& x, int heads) {
+    const int row = threadIdx.x / kLanes;
+    t = row / heads;
+    h = row - t * heads;
+    e = (int64_t)t * x.row_stride + (int64_t)h * x.head_stride + threadIdx.x % kLanes * 8;
+  }
+  __device__ __forceinline__ void next(const KvRows& x, int heads) {
+    const int dt = kRows / heads, dh = kRows - dt * heads;
+    t += dt;
+    h += dh;
+    e += (int64_t)dt * x.row_stride + (int64_t)dh * x.head_stride;
+    if (h >= heads) {
+      h -= heads;
+      t += 1;
+      e += x.row_stride - (int64_t)heads * x.head_stride;
+    }
+  }
+};
+
+// grid.x: blocks of `tokens` tokens; grid.y: 0 keys, 1 values.  U passes' loads
+// are in flight together.
+template <int BITS, int D, int G, int DT, int U>
+__global__ __launch_bounds__(kThreads) void k_kv_write(KvCache c, KvBatch b, KvRows k, KvRows v, int tokens) {
+  using R = Rows<D>;
+  __shared__ int64_t place[kMaxTokens];
+  const bool values = blockIdx.y == 1;
+  const KvRows& in = values ? v : k;
+  uint8_t* const out_codes = values ? c.v_codes : c.k_codes;
+  uint32_t* const out_params = values ? c.v_params : c.k_params;
+  const int t0 = blockIdx.x * tokens, count = min(tokens, b.rows - t0);
+  const void* from = static_cast<const uint8_t*>(in.p) + (int64_t)t0 * in.row_stride * (DT == kKvF32 ? 4 : 2);
+  const int run = threadIdx.x % R::kLanes;
+  const int at_codes = values ? value_place<BITS, D>(run) : key_run<D>(run) * BITS;
+  R load(in, c.kv_heads), store = load;
+  bool looked_up = false;
+  for (int r0 = 0; r0 < count * c.kv_heads; r0 += U * R::kRows) {
+    u32x4 raw[U][DT == kKvF32 ? 2 : 1];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (u32x4& w : raw[u]) w = u32x4{0, 0, 0, 0};
+      if (load.t < count) load8<DT>(from, load.e, raw[u]);
+      load.next(in, c.kv_heads);
+    }
+    if (!looked_up) {   // behind the first loads
+      look_up(c, b, t0, count, place);
+      __syncthreads();
+      looked_up = true;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float x[8];
+      widen8<DT>(raw[u], x);
+      float mn = x[0], mx = x[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) {
+        mn = fminf(mn, x[i]);
+        mx = fmaxf(mx, x[i]);
+      }
+      run_minmax<G / 8>(mn, mx);
+      const QParams q = group_params_fast<BITS>(mn, mx);
+      uint32_t w[BITS / 4];
+      encode8<BITS>(x, q, w);
+      if (values) transpose_values<BITS, D>(w);   // every lane of a row takes part
+      const int64_t at0 = store.t < count ? place[store.t] : -1;
+      if (at0 >= 0) {
+        const int64_t at = at0 + ((int64_t)store.h << c.page_shift);
+        store_codes<BITS, D>(out_codes + at * (D * BITS / 8), at_codes, values, w);
+        if (run % (G / 8) == 0) out_params[at * (D / G) + run / (G / 8)] = q.word;
+      }
+      store.next(in, c.kv_heads);
+    }
+  }
+}
+
+template <int BITS, int D, int G, int DT, int U>
+__global__ __launch_bounds__(kThreads) void k_kv_read(KvCache c, KvBatch b, KvRows k, KvRows v, int tokens) {
+  using R = Rows<D>;
+  __shared__ int64_t place[kMaxTokens];
   const bool values = blockIdx.y == 1;
   const KvRows& out = values ? v : k;
-  const L l = lane_of<D>(c.kv_heads);
-  const int seq = lane_seq<D>(b, l);
-  if (l.t >= b.rows) return;
-  const RowSlot s = row_slot(c, b, seq, l.t);
-  if (s.page < 0) return;
-  const int64_t r = ((s.page * c.kv_heads + l.h) << c.page_shift) + s.slot;
-  const uint8_t* codes = (values ? c.v_codes : c.k_codes) + r * (D * BITS / 8);
-  const uint32_t word = (values ? c.v_params : c.k_params)[r * (D / G) + l.run / (G / 8)];
-  uint32_t code[8];
-  if (values) {
-    // elements 8 run + i = tile run/2, column 8 (run % 2) + i: one code of each of 8 lanes' shares
-    constexpr int kUnitBytes = D * BITS / 8 / 16;
-    const int tile = l.run / 2, col = (l.run % 2) * 8;
+  const uint8_t* const in_codes = values ? c.v_codes : c.k_codes;
+  const uint32_t* const in_params = values ? c.v_params : c.k_params;
+  const int t0 = blockIdx.x * tokens, count = min(tokens, b.rows - t0);
+  void* to = static_cast<uint8_t*>(out.p) + (int64_t)t0 * out.row_stride * (DT == kKvF32 ? 4 : 2);
+  const int run = threadIdx.x % R::kLanes;
+  const int at_codes = values ? value_place<BITS, D>(run) : key_run<D>(run) * BITS;
+  R load(out, c.kv_heads), store = load;
+  look_up(c, b, t0, count, place);
+  __syncthreads();
+  for (int r0 = 0; r0 < count * c.kv_heads; r0 += U * R::kRows) {
+    uint32_t w[U][BITS / 4], word[U];
+    bool there[U];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t byte = codes[(col + i) * kUnitBytes + tile * BITS / 8];
-      code[i] = BITS == 8 ? byte : (tile & 1 ? byte >> 4 : byte & 15u);
+    for (int u = 0; u < U; ++u) {
+      const int64_t at0 = load.t < count ? place[load.t] : -1;
+      there[u] = at0 >= 0;
+      word[u] = 0;
+#pragma unroll
+      for (uint32_t& i : w[u]) i = 0;
+      if (there[u]) {
+        const int64_t at = at0 + ((int64_t)load.h << c.page_shift);
+        load_codes<BITS, D>(in_codes + at * (D * BITS / 8), at_codes, values, w[u]);
+        word[u] = in_params[at * (D / G) + run / (G / 8)];
+      }
+      load.next(out, c.kv_heads);
     }
-  } else if constexpr (BITS == 4) {
-    const uint32_t w = reinterpret_cast<const uint32_t*>(codes)[key_run<D>(l.run)];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) code[i] = (w >> (4 * i)) & 15u;
-  } else {
-    const u32x2 w = reinterpret_cast<const u32x2*>(codes)[key_run<D>(l.run)];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) code[i] = (w[i / 4] >> (8 * (i % 4))) & 255u;
+    for (int u = 0; u < U; ++u) {
+      if (values) transpose_values<BITS, D>(w[u]);
+      float x[8];
+      decode8<BITS>(w[u], word[u], x);
+      if (there[u]) store8<DT>(to, store.e, x);
+      store.next(out, c.kv_heads);
+    }
   }
-  const float sf = f16_to_f32(word & 0xffffu), zf = f16_to_f32(word >> 16);
-  float x[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = fmaf((float)code[i], sf, zf);
-  store8<DT>(out.p, (int64_t)l.t * out.row_stride + (int64_t)l.h * out.head_stride + l.run * 8, x);
 }
 
 }  // namespace kv
@@ -247,24 +414,32 @@ hipError_t with_form(const KvCache& c, int dtype, F&& f) {
   return c.bits == 4 ? with_dim(IC<4>{}) : with_dim(IC<8>{});
 }
 
-unsigned row_blocks(const KvWriteArgs& a) {
-  const int64_t rows = (int64_t)a.b.rows * a.c.kv_heads, per = kv::kThreads / (a.c.head_dim / 8);
-  return (unsigned)((rows + per - 1) / per);
+// Tokens of a block: about 256 rows, fewer while that leaves compute units idle.
+int block_tokens(const KvWriteArgs& a) {
+  int64_t tokens = 256 / a.c.kv_heads;
+  const int64_t spread = ((int64_t)a.b.rows + 511) / 512;
+  if (tokens > spread) tokens = spread;
+  if (tokens > kv::kMaxTokens) tokens = kv::kMaxTokens;
+  return (int)(tokens < 1 ? 1 : tokens);
 }
+
+constexpr int kPasses = 4;   // rows of a lane in flight together
 
 }  // namespace
 
 hipError_t run_kv_write(const KvWriteArgs& a, hipStream_t st) {
+  const int tokens = block_tokens(a);
   return with_form(a.c, a.k.dtype, [&](auto B, auto D, auto G, auto T) {
-    return kv_launch(kv::k_kv_write<B(), D(), G(), T()>, dim3(row_blocks(a), 2), dim3(kv::kThreads), st,
-                     a.c, a.b, a.k, a.v);
+    return kv_launch(kv::k_kv_write<B(), D(), G(), T(), kPasses>, dim3((a.b.rows + tokens - 1) / tokens, 2),
+                     dim3(kv::kThreads), st, a.c, a.b, a.k, a.v, tokens);
   });
 }
 
 hipError_t run_kv_read(const KvWriteArgs& a, hipStream_t st) {
+  const int tokens = block_tokens(a);
   return with_form(a.c, a.k.dtype, [&](auto B, auto D, auto G, auto T) {
-    return kv_launch(kv::k_kv_read<B(), D(), G(), T()>, dim3(row_blocks(a), 2), dim3(kv::kThreads), st,
-                     a.c, a.b, a.k, a.v);
+    return kv_launch(kv::k_kv_read<B(), D(), G(), T(), kPasses>, dim3((a.b.rows + tokens - 1) / tokens, 2),
+                     dim3(kv::kThreads), st, a.c, a.b, a.k, a.v, tokens);
   });
 }
 

@@ -70,7 +70,7 @@ KvPlan kv_attention_plan(const KvCache& c, const KvBatch& b, int heads_per_kv, i
   p.row_blocks = (int32_t)((rows + block_rows - 1) / block_rows);
   int64_t span = b.max_len;
   if (causal && window > 0) {
-    const int64_t seen = (int64_t)window + block_rows / heads_per_kv + 1 + sinks + 2 * 32;
+    const int64_t seen = (int64_t)window + block_rows / heads_per_kv + 1 + sinks + 4 * 32;   // and the tiles that are cut
     span = seen < span ? seen : span;
   }
   const int64_t tiles = (span + 31) / 32 > 0 ? (span + 31) / 32 : 1;
