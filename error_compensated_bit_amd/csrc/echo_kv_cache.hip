@@ -221,9 +221,9 @@ __device__ __forceinline__ void load_codes(const uint8_t* row, int place, bool v
     }
   }
   if constexpr (BITS == 4) {
-    w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(row + place));
+    w[0] = *reinterpret_cast<const uint32_t*>(row + place);
   } else {
-    const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(row + place));
+    const u32x2 v = *reinterpret_cast<const u32x2*>(row + place);
     w[0] = v.x;
     w[1] = v.y;
   }
@@ -259,30 +259,32 @@ __device__ __forceinline__ void look_up(const KvCache& c, const KvBatch& b, int 
   place[wave * 64 + threadIdx.x % 64] = s.page < 0 ? -1 : ((s.page * c.kv_heads) << c.page_shift) + s.slot;
 }
 
-// Rows (token, head) of a block, token-major: lane `run` of D/8 lanes has 8
-// consecutive elements of a row; a pass covers kRows rows of the block, and
-// token, head and offset move from pass to pass by additions.
+// Rows (token, head) of a block, head-major: neighbouring rows are neighbours in
+// the cache, whose short rows share lines.  Lane `run` of D/8 lanes has 8
+// consecutive elements of a row; a pass covers kRows rows of the block's
+// `tokens` * heads, and token, head and offset move from pass to pass by
+// additions.
 template <int D>
 struct Rows {
   static constexpr int kLanes = D / 8;
   static constexpr int kRows = kThreads / kLanes;
   int t, h;            // token of the block, head
   int64_t e;           // element offset of the lane's elements from the block's first row
-  __device__ __forceinline__ Rows(const KvRows& x, int heads) {
+  __device__ __forceinline__ Rows(const KvRows& x, int tokens) {
     const int row = threadIdx.x / kLanes;
-    t = row / heads;
-    h = row - t * heads;
+    h = row / tokens;
+    t = row - h * tokens;
     e = (int64_t)t * x.row_stride + (int64_t)h * x.head_stride + threadIdx.x % kLanes * 8;
   }
-  __device__ __forceinline__ void next(const KvRows& x, int heads) {
-    const int dt = kRows / heads, dh = kRows - dt * heads;
+  __device__ __forceinline__ void next(const KvRows& x, int tokens) {
+    const int dh = kRows / tokens, dt = kRows - dh * tokens;
     t += dt;
     h += dh;
     e += (int64_t)dt * x.row_stride + (int64_t)dh * x.head_stride;
-    if (h >= heads) {
-      h -= heads;
-      t += 1;
-      e += x.row_stride - (int64_t)heads * x.head_stride;
+    if (t >= tokens) {
+      t -= tokens;
+      h += 1;
+      e += x.head_stride - (int64_t)tokens * x.row_stride;
     }
   }
 };
@@ -301,16 +303,16 @@ __global__ __launch_bounds__(kThreads) void k_kv_write(KvCache c, KvBatch b, KvR
   const void* from = static_cast<const uint8_t*>(in.p) + (int64_t)t0 * in.row_stride * (DT == kKvF32 ? 4 : 2);
   const int run = threadIdx.x % R::kLanes;
   const int at_codes = values ? value_place<BITS, D>(run) : key_run<D>(run) * BITS;
-  R load(in, c.kv_heads), store = load;
+  R load(in, tokens), store = load;
   bool looked_up = false;
-  for (int r0 = 0; r0 < count * c.kv_heads; r0 += U * R::kRows) {
+  for (int r0 = 0; r0 < tokens * c.kv_heads; r0 += U * R::kRows) {
     u32x4 raw[U][DT == kKvF32 ? 2 : 1];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
 #pragma unroll
       for (u32x4& w : raw[u]) w = u32x4{0, 0, 0, 0};
-      if (load.t < count) load8<DT>(from, load.e, raw[u]);
-      load.next(in, c.kv_heads);
+      if (load.t < count && load.h < c.kv_heads) load8<DT>(from, load.e, raw[u]);
+      load.next(in, tokens);
     }
     if (!looked_up) {   // behind the first loads
       look_up(c, b, t0, count, place);
@@ -332,13 +334,13 @@ __global__ __launch_bounds__(kThreads) void k_kv_write(KvCache c, KvBatch b, KvR
       uint32_t w[BITS / 4];
       encode8<BITS>(x, q, w);
       if (values) transpose_values<BITS, D>(w);   // every lane of a row takes part
-      const int64_t at0 = store.t < count ? place[store.t] : -1;
+      const int64_t at0 = store.t < count && store.h < c.kv_heads ? place[store.t] : -1;
       if (at0 >= 0) {
         const int64_t at = at0 + ((int64_t)store.h << c.page_shift);
         store_codes<BITS, D>(out_codes + at * (D * BITS / 8), at_codes, values, w);
         if (run % (G / 8) == 0) out_params[at * (D / G) + run / (G / 8)] = q.word;
       }
-      store.next(in, c.kv_heads);
+      store.next(in, tokens);
     }
   }
 }
@@ -355,15 +357,15 @@ __global__ __launch_bounds__(kThreads) void k_kv_read(KvCache c, KvBatch b, KvRo
   void* to = static_cast<uint8_t*>(out.p) + (int64_t)t0 * out.row_stride * (DT == kKvF32 ? 4 : 2);
   const int run = threadIdx.x % R::kLanes;
   const int at_codes = values ? value_place<BITS, D>(run) : key_run<D>(run) * BITS;
-  R load(out, c.kv_heads), store = load;
+  R load(out, tokens), store = load;
   look_up(c, b, t0, count, place);
   __syncthreads();
-  for (int r0 = 0; r0 < count * c.kv_heads; r0 += U * R::kRows) {
+  for (int r0 = 0; r0 < tokens * c.kv_heads; r0 += U * R::kRows) {
     uint32_t w[U][BITS / 4], word[U];
     bool there[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t at0 = load.t < count ? place[load.t] : -1;
+      const int64_t at0 = load.t < count && load.h < c.kv_heads ? place[load.t] : -1;
       there[u] = at0 >= 0;
       word[u] = 0;
 #pragma unroll
@@ -373,7 +375,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_read(KvCache c, KvBatch b, KvRo
         load_codes<BITS, D>(in_codes + at * (D * BITS / 8), at_codes, values, w[u]);
         word[u] = in_params[at * (D / G) + run / (G / 8)];
       }
-      load.next(out, c.kv_heads);
+      load.next(out, tokens);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -381,7 +383,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_read(KvCache c, KvBatch b, KvRo
       float x[8];
       decode8<BITS>(w[u], word[u], x);
       if (there[u]) store8<DT>(to, store.e, x);
-      store.next(out, c.kv_heads);
+      store.next(out, tokens);
     }
   }
 }
