@@ -150,8 +150,7 @@ int cache_rows(const echo_kv_cache* cache, const echo_kv_batch* batch, const ech
   if ((rc = check_form(cache)) || (rc = check_batch_sizes(batch))) return rc;
   if (!k || !v) return ECHO_ERR_ARG;
   if (k->dtype != v->dtype) return ECHO_ERR_ARG;
-  const int64_t per_block = 256 / (cache->head_dim / 8);
-  if (((int64_t)batch->rows * cache->kv_heads + per_block - 1) / per_block > kMaxBlocks) return ECHO_ERR_SHAPE;
+  if (kv_cache_blocks(cache_of(cache), batch_of(batch)) > kMaxBlocks) return ECHO_ERR_SHAPE;
   if (batch->rows == 0 || batch->seqs == 0) return ECHO_OK;
   if ((rc = check_cache(cache)) || (rc = check_batch(batch))) return rc;
   if ((rc = check_rows(k, batch->rows, cache->kv_heads, cache->head_dim, true, out))) return rc;

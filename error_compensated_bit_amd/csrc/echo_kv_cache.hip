@@ -83,14 +83,14 @@ __device__ __forceinline__ void store8(void* p, int64_t e, const float* v) {
   }
 }
 
-// Group parameters (see group_params): the same results without the compiler's
-// full divisions, which cost a fifth of the kernel's instructions.  span / qmax
+// Group parameters: the all-reduce quantizer's, without the compiler's full
+// divisions, which cost a fifth of the kernel's instructions.  span / qmax
 // is the product with the rounded reciprocal and one correction, which rounds
 // correctly wherever the quotient does not vanish in fp16 (below 2^-25 it is 0
 // either way); spans beyond 65504 qmax give 65504.  1 / step is the hardware's
 // reciprocal and one correction; it is right for every fp16 step.
 template <int BITS>
-__device__ __forceinline__ QParams group_params_fast(float mn, float mx) {
+__device__ __forceinline__ QParams group_params(float mn, float mx) {
   constexpr float qmax = (float)((1 << BITS) - 1);
   constexpr float rq = 1.0f / qmax;
   const float zc = fminf(fmaxf(mn, -65504.0f), 65504.0f);
@@ -237,26 +237,28 @@ __device__ __forceinline__ int key_run(int r) {
 
 constexpr int kMaxTokens = 256;   // of a block
 
-// A block's tokens t0 .. t0 + count - 1: for each, the index of its row of head
-// 0 in the cache, -1 where it has no place.  A wave looks up 64 tokens: their
-// first and last sequence together, and each lane's own between the two by
-// bisection.  Looking places up once per token and block keeps the chain of
-// dependent loads out of the rows' way.
+// A block's tokens t0 .. t0 + count - 1: for each, its row of head 0 in the
+// cache, -1 where it has no place.  A wave looks up 64 tokens, mostly of one
+// sequence; where they are not, each lane finds its own by bisection.  Looking
+// places up once per token and block keeps the chain of dependent loads out of
+// the rows' way.
 __device__ __forceinline__ void look_up(const KvCache& c, const KvBatch& b, int t0, int count, int64_t* place) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   if (wave * 64 >= count) return;
   const int first = t0 + wave * 64, last = min(first + 63, t0 + count - 1);
   const int t = min(first + (int)(threadIdx.x % 64), last);
-  int lo = seq_of_row(b.row_start, b.seqs, first);
-  int hi = first == last ? lo : seq_of_row(b.row_start, b.seqs, last);
-  if (lo < 0) lo = 0;
-  while (lo < hi) {
-    const int mid = lo + (hi - lo + 1) / 2;
-    if (b.row_start[mid] <= t) lo = mid;
-    else hi = mid - 1;
+  SeqEntry s = seq_of_row(b, first);
+  if (s.seq < 0 || last >= s.end) {
+    int lo = s.seq < 0 ? 0 : s.seq, hi = seq_of_row(b, last).seq;
+    const bool any = hi >= 0;
+    while (lo < hi) {
+      const int mid = lo + (hi - lo + 1) / 2;
+      if (b.row_start[mid] <= t) lo = mid;
+      else hi = mid - 1;
+    }
+    if (any) s = SeqEntry{lo, b.row_start[lo], b.row_start[lo + 1], b.kv_len[lo]};
   }
-  const RowSlot s = row_slot(c, b, hi < 0 ? -1 : lo, t);
-  place[wave * 64 + threadIdx.x % 64] = s.page < 0 ? -1 : ((s.page * c.kv_heads) << c.page_shift) + s.slot;
+  place[wave * 64 + threadIdx.x % 64] = row_place(c, b, s, t);
 }
 
 // Rows (token, head) of a block, head-major: neighbouring rows are neighbours in
@@ -330,7 +332,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_write(KvCache c, KvBatch b, KvR
         mx = fmaxf(mx, x[i]);
       }
       run_minmax<G / 8>(mn, mx);
-      const QParams q = group_params_fast<BITS>(mn, mx);
+      const QParams q = group_params<BITS>(mn, mx);
       uint32_t w[BITS / 4];
       encode8<BITS>(x, q, w);
       if (values) transpose_values<BITS, D>(w);   // every lane of a row takes part
@@ -417,9 +419,9 @@ hipError_t with_form(const KvCache& c, int dtype, F&& f) {
 }
 
 // Tokens of a block: about 256 rows, fewer while that leaves compute units idle.
-int block_tokens(const KvWriteArgs& a) {
-  int64_t tokens = 256 / a.c.kv_heads;
-  const int64_t spread = ((int64_t)a.b.rows + 511) / 512;
+int block_tokens(const KvCache& c, const KvBatch& b) {
+  int64_t tokens = 256 / c.kv_heads;
+  const int64_t spread = ((int64_t)b.rows + 511) / 512;
   if (tokens > spread) tokens = spread;
   if (tokens > kv::kMaxTokens) tokens = kv::kMaxTokens;
   return (int)(tokens < 1 ? 1 : tokens);
@@ -429,18 +431,23 @@ constexpr int kPasses = 4;   // rows of a lane in flight together
 
 }  // namespace
 
+int64_t kv_cache_blocks(const KvCache& c, const KvBatch& b) {
+  const int tokens = block_tokens(c, b);
+  return ((int64_t)b.rows + tokens - 1) / tokens;
+}
+
 hipError_t run_kv_write(const KvWriteArgs& a, hipStream_t st) {
-  const int tokens = block_tokens(a);
+  const int tokens = block_tokens(a.c, a.b);
   return with_form(a.c, a.k.dtype, [&](auto B, auto D, auto G, auto T) {
-    return kv_launch(kv::k_kv_write<B(), D(), G(), T(), kPasses>, dim3((a.b.rows + tokens - 1) / tokens, 2),
+    return kv_launch(kv::k_kv_write<B(), D(), G(), T(), kPasses>, dim3((unsigned)kv_cache_blocks(a.c, a.b), 2),
                      dim3(kv::kThreads), st, a.c, a.b, a.k, a.v, tokens);
   });
 }
 
 hipError_t run_kv_read(const KvWriteArgs& a, hipStream_t st) {
-  const int tokens = block_tokens(a);
+  const int tokens = block_tokens(a.c, a.b);
   return with_form(a.c, a.k.dtype, [&](auto B, auto D, auto G, auto T) {
-    return kv_launch(kv::k_kv_read<B(), D(), G(), T(), kPasses>, dim3((a.b.rows + tokens - 1) / tokens, 2),
+    return kv_launch(kv::k_kv_read<B(), D(), G(), T(), kPasses>, dim3((unsigned)kv_cache_blocks(a.c, a.b), 2),
                      dim3(kv::kThreads), st, a.c, a.b, a.k, a.v, tokens);
   });
 }

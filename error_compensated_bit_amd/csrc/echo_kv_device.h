@@ -43,67 +43,50 @@ struct QParams {
   uint32_t word;  // step bits | zero bits << 16
 };
 
-template <int BITS>
-__device__ __forceinline__ QParams group_params(float mn, float mx) {
-  constexpr float qmax = (float)((1 << BITS) - 1);
-  const float zc = fminf(fmaxf(mn, -65504.0f), 65504.0f);
-  uint32_t zb = f32_to_f16(zc);
-  zb = (zb == 0x8000u) ? 0u : zb;
-  const float zf = f16_to_f32(zb);
-  float s = (mx - zf) / qmax;
-  s = (s > 0.0f) ? fminf(s, 65504.0f) : 0.0f;
-  const uint32_t sb = f32_to_f16(s);
-  const float sf = f16_to_f32(sb);
-  const float inv = (sf > 0.0f) ? 1.0f / sf : 0.0f;
-  return QParams{zf, sf, inv, sb | (zb << 16)};
-}
+// A sequence and its entries of the batch's arrays; seq < 0: none.
+struct SeqEntry {
+  int seq, start, end, len;
+};
 
-template <int BITS>
-__device__ __forceinline__ uint32_t encode(float v, const QParams& q) {
-  constexpr float qmax = (float)((1 << BITS) - 1);
-  const float t = (v - q.zf) * q.inv;
-  return (uint32_t)fminf(fmaxf(rintf(t), 0.0f), qmax);
-}
-
-// Largest b in [0, seqs) with row_start[b] <= t, -1 if there is none; t is the
-// same in all lanes, and 64 candidates are looked at per step, so that up to
-// 64 sequences cost one load.  Ends for any contents of row_start.
-__device__ __forceinline__ int seq_of_row(const int32_t* __restrict__ row_start, int seqs, int t) {
+// The largest seq with row_start[seq] <= t; t is the same in all lanes, and 64
+// candidates are looked at per step, in the last step with all their entries,
+// so that up to 64 sequences cost one round of loads.  Ends for any contents.
+__device__ __forceinline__ SeqEntry seq_of_row(const KvBatch& b, int t) {
   const int lane = threadIdx.x % 64;
-  int lo = 0, hi = seqs;
-  for (;;) {
+  int lo = 0, hi = b.seqs;
+  while (hi - lo > 64) {
     const int stride = (hi - lo + 63) / 64;
     const int64_t i = (int64_t)lo + (int64_t)lane * stride;
-    const bool le = i < hi && row_start[i] <= t;
-    const int c = __popcll(__ballot(le));
-    if (c == 0) return lo > 0 ? lo : -1;
+    const int c = __popcll(__ballot(i < hi && b.row_start[i] <= t));
+    if (c == 0) break;
     lo += (c - 1) * stride;
-    if (stride == 1) return lo;
     hi = lo + stride < hi ? lo + stride : hi;
   }
+  int start = 0, end = 0, len = 0;
+  const bool mine = lane < hi - lo;
+  if (mine) {
+    start = b.row_start[lo + lane];
+    end = b.row_start[lo + lane + 1];
+    len = b.kv_len[lo + lane];
+  }
+  const int c = __popcll(__ballot(mine && start <= t));
+  const int at = c == 0 ? 0 : c - 1;
+  return SeqEntry{c == 0 ? -1 : lo + at, __builtin_amdgcn_readlane(start, at), __builtin_amdgcn_readlane(end, at),
+                  __builtin_amdgcn_readlane(len, at)};
 }
 
-// Slot of row t of the packed arrays in one head's plane of a page, or
-// page < 0 where the row has none: rows outside every sequence, positions
-// outside the page table, entries that name no page.
-struct RowSlot {
-  int64_t page;
-  int32_t slot;
-};
-__device__ __forceinline__ RowSlot row_slot(const KvCache& c, const KvBatch& b, int seq, int t) {
-  RowSlot r{-1, 0};
-  if (seq < 0 || t < b.row_start[seq]) return r;
-  const int end = b.row_start[seq + 1];
-  if (t >= end) return r;
-  const int64_t pos = (int64_t)b.kv_len[seq] - end + t;
-  if (pos < 0 || pos >= b.max_len) return r;
+// Row of head 0 in the cache that row t of the packed arrays belongs to, or -1
+// where it has no place: rows outside every sequence, positions outside the
+// page table, entries that name no page.
+__host__ __device__ __forceinline__ int64_t row_place(const KvCache& c, const KvBatch& b, const SeqEntry& s, int t) {
+  if (s.seq < 0 || t < s.start || t >= s.end) return -1;
+  const int64_t pos = (int64_t)s.len - s.end + t;
+  if (pos < 0 || pos >= b.max_len) return -1;
   const int64_t pi = pos >> c.page_shift;
-  if (pi >= b.table_stride) return r;
-  const int64_t page = b.page_table[(int64_t)seq * b.table_stride + pi];
-  if (page < 0 || page >= c.num_pages) return r;
-  r.page = page;
-  r.slot = (int)(pos & ((1 << c.page_shift) - 1));
-  return r;
+  if (pi >= b.table_stride) return -1;
+  const int64_t page = b.page_table[(int64_t)s.seq * b.table_stride + pi];
+  if (page < 0 || page >= c.num_pages) return -1;
+  return ((page * c.kv_heads) << c.page_shift) + (pos & ((1 << c.page_shift) - 1));
 }
 
 // ---- shared by the attention kernel and the one that joins its splits
@@ -116,11 +99,11 @@ constexpr float kLowest = -3.0e38f;  // running maximum before any key: below ev
 // and the earliest row's window.
 struct Span {
   int t1, start, tiles;
-  __device__ __forceinline__ int token(int t) const { return t < t1 ? t * kTile : start + (t - t1) * kTile; }
+  __host__ __device__ __forceinline__ int token(int t) const { return t < t1 ? t * kTile : start + (t - t1) * kTile; }
 };
 
 // What the rows of tokens i0 .. i1 (of n new ones) see of a sequence of `len` keys.
-__device__ __forceinline__ Span key_span(const KvAttnArgs& a, int len, int n, int i0, int i1) {
+__host__ __device__ __forceinline__ Span key_span(const KvAttnArgs& a, int len, int n, int i0, int i1) {
   Span s{0, 0, 0};
   int end = len;
   if (a.causal) {
@@ -148,7 +131,7 @@ __device__ __forceinline__ Span key_span(const KvAttnArgs& a, int len, int n, in
 struct Seq {
   int first, n, computed, len;
 };
-__device__ __forceinline__ Seq sequence(const KvAttnArgs& a, int b) {
+__host__ __device__ __forceinline__ Seq sequence(const KvAttnArgs& a, int b) {
   Seq s;
   int lo = a.b.row_start[b], hi = a.b.row_start[b + 1];
   lo = lo < 0 ? 0 : lo > a.b.rows ? a.b.rows : lo;
@@ -164,7 +147,7 @@ __device__ __forceinline__ Seq sequence(const KvAttnArgs& a, int b) {
 }
 
 // One (m, l) pair and one output row of D floats of every split of a query row.
-__device__ __forceinline__ int64_t part_index(const KvAttnArgs& a, int b, int hk, int prows, int row, int split) {
+__host__ __device__ __forceinline__ int64_t part_index(const KvAttnArgs& a, int b, int hk, int prows, int row, int split) {
   return (((int64_t)b * a.c.kv_heads + hk) * prows + row) * a.plan.splits + split;
 }
 

@@ -66,6 +66,8 @@ struct KvAttnArgs {
 // Each returns the first launch error (hipSuccess when every launch went out).
 hipError_t run_kv_write(const KvWriteArgs& a, hipStream_t st);
 hipError_t run_kv_read(const KvWriteArgs& a, hipStream_t st);
+// Blocks along x of both.
+int64_t kv_cache_blocks(const KvCache& c, const KvBatch& b);
 hipError_t run_kv_attention(const KvAttnArgs& a, hipStream_t st);
 
 // The attention kernel of one code width and head size (a translation unit of its own).
