@@ -232,7 +232,46 @@ struct QueryRows {
   f16x8 op[ROWS / 16][kSlices][64];
   float rf[ROWS], qs[ROWS][kGroups];
 
-  // Rows row0 .. row0 + ROWS - 1 of a (sequence, K/V head) with `rows` rows; those behind the last are 0.
+  // Elements `run` of row row0 + r of a (sequence, K/V head) with `rows` rows; 0 behind the last.
+  __device__ __forceinline__ u32x4 load(const KvAttnArgs& a, const Seq& sq, int hk, int row, int rows, int run) const {
+    if (row >= rows) return u32x4{0, 0, 0, 0};
+    const int i = row / a.heads_per_kv, h = row - i * a.heads_per_kv;
+    return *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.q.p) + (int64_t)(sq.first + i) * a.q.row_stride +
+                                           (int64_t)(hk * a.heads_per_kv + h) * a.q.head_stride + run * 8);
+  }
+  static __device__ __forceinline__ void widen(u32x4 raw, int dtype, float* x) {
+    if (dtype == kKvF16) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = f16_to_f32(j & 1 ? raw[j / 2] >> 16 : raw[j / 2] & 0xffffu);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(j & 1 ? raw[j / 2] & 0xffff0000u : raw[j / 2] << 16);
+    }
+  }
+  // Elements x of a row, times 2^up, to their places.
+  __device__ __forceinline__ void put(const float* x, int up, int r, int run) {
+    _Float16 e[8];
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      e[j] = (_Float16)ldexpf(x[j], up);
+      sum += (float)e[j];
+    }
+    sum = run_reduce<G / 8>(sum, [](float u, float v) { return u + v; });
+    f16x8 o;
+    if constexpr (BITS == 4) {
+      const _Float16 low = (_Float16)0.0625f;   // codes one nibble higher count 16 times
+      o = f16x8{e[0], e[4], e[1] * low, e[5] * low, e[2], e[6], e[3] * low, e[7] * low};
+    } else {
+      o = f16x8{e[0], e[2], e[1], e[3], e[4], e[6], e[5], e[7]};
+    }
+    op[r / 16][run / 4][run % 4 * 16 + r % 16] = o;
+    if (run % (G / 8) == 0) qs[r][run / (G / 8)] = sum * 0x1p-24f;
+  }
+
+  // Rows row0 .. row0 + ROWS - 1, each with its own power of two: the row's
+  // largest element comes into [2^14, 2^15), and bf16 values keep all their
+  // bits down to 2^-24 of the largest.
   template <int THREADS>
   __device__ __forceinline__ void stage(const KvAttnArgs& a, const Seq& sq, int hk, int row0, int rows) {
     static_assert(ROWS * kRuns % 64 == 0, "whole waves");
@@ -240,48 +279,56 @@ struct QueryRows {
     for (int pass = 0; pass * THREADS < ROWS * kRuns; ++pass) {
       const int unit = pass * THREADS + threadIdx.x, r = unit / kRuns, run = unit % kRuns;
       if (unit >= ROWS * kRuns) break;
-      const int row = row0 + r;
-      u32x4 raw = {0, 0, 0, 0};
-      if (row < rows) {
-        const int i = row / a.heads_per_kv, h = row - i * a.heads_per_kv;
-        raw = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.q.p) +
-                                              (int64_t)(sq.first + i) * a.q.row_stride +
-                                              (int64_t)(hk * a.heads_per_kv + h) * a.q.head_stride + run * 8);
-      }
       float x[8], top = 0.0f;
-      if (a.q.dtype == kKvF16) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = f16_to_f32(j & 1 ? raw[j / 2] >> 16 : raw[j / 2] & 0xffffu);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(j & 1 ? raw[j / 2] & 0xffff0000u : raw[j / 2] << 16);
-      }
+      widen(load(a, sq, hk, row0 + r, rows, run), a.q.dtype, x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
       top = run_reduce<kRuns>(top, [](float u, float v) { return fmaxf(u, v); });
-      // a power of two takes the row's largest element into [2^14, 2^15): bf16
-      // values keep all their bits down to 2^-24 of the largest
       const int field = (int)(__float_as_uint(top) >> 23);
       const int up = field == 0 || field == 255 ? 0 : 14 - (field - 127);
-      _Float16 e[8];
-      float sum = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        e[j] = (_Float16)ldexpf(x[j], up);
-        sum += (float)e[j];
-      }
-      sum = run_reduce<G / 8>(sum, [](float u, float v) { return u + v; });
-      f16x8 o;
-      if constexpr (BITS == 4) {
-        const _Float16 low = (_Float16)0.0625f;   // codes one nibble higher count 16 times
-        o = f16x8{e[0], e[4], e[1] * low, e[5] * low, e[2], e[6], e[3] * low, e[7] * low};
-      } else {
-        o = f16x8{e[0], e[2], e[1], e[3], e[4], e[6], e[5], e[7]};
-      }
-      op[r / 16][run / 4][run % 4 * 16 + r % 16] = o;
+      put(x, up, r, run);
       if (run == 0) rf[r] = ldexpf(a.scale_log2, 24 - up);
-      if (run % (G / 8) == 0) qs[r][run / (G / 8)] = sum * 0x1p-24f;
     }
+  }
+
+  // All rows with one power of two, from the largest finite element of the
+  // block (a row 2^14 times smaller than another still keeps bf16's bits);
+  // returns the factor from raw scores to log2 units.  top: a float per wave.
+  template <int THREADS>
+  __device__ __forceinline__ float stage_together(const KvAttnArgs& a, const Seq& sq, int hk, int row0, int rows,
+                                                  float* tops) {
+    constexpr int kPasses = ROWS * kRuns / THREADS;
+    static_assert(ROWS * kRuns % THREADS == 0, "whole passes");
+    u32x4 raw[kPasses];
+#pragma unroll
+    for (int pass = 0; pass < kPasses; ++pass) {
+      const int unit = pass * THREADS + threadIdx.x;
+      raw[pass] = load(a, sq, hk, row0 + unit / kRuns, rows, unit % kRuns);
+    }
+    float top = 0.0f;
+#pragma unroll
+    for (int pass = 0; pass < kPasses; ++pass) {
+      float x[8];
+      widen(raw[pass], a.q.dtype, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fabsf(x[j]) < INFINITY ? fmaxf(top, fabsf(x[j])) : top;
+    }
+#pragma unroll
+    for (int i = 1; i < 64; i *= 2) top = fmaxf(top, __shfl_xor(top, i));
+    tops[threadIdx.x / 64] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < THREADS / 64; ++i) top = fmaxf(top, tops[i]);
+    const int field = __builtin_amdgcn_readfirstlane((int)(__float_as_uint(top) >> 23));
+    const int up = field == 0 ? 0 : 14 - (field - 127);
+#pragma unroll
+    for (int pass = 0; pass < kPasses; ++pass) {
+      const int unit = pass * THREADS + threadIdx.x;
+      float x[8];
+      widen(raw[pass], a.q.dtype, x);
+      put(x, up, unit / kRuns, unit % kRuns);
+    }
+    return ldexpf(a.scale_log2, 24 - up);
   }
 };
 
@@ -379,11 +426,13 @@ struct Wave {
       }
     }
     if (masked) {
+      int from = tb;
+      asm volatile("" : "+s"(from));   // the comparisons stay in this branch
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int j = tb + 16 * s + quad * 4 + r;
+          const int j = from + 16 * s + quad * 4 + r;
           const bool there = j < len && (ok >> s & 1u);
 #pragma unroll
           for (int t = 0; t < NT; ++t)
@@ -689,34 +738,48 @@ __global__ __launch_bounds__(NW * 64, few_min_waves(D, NT)) void k_kv_attention_
 }
 
 // ------------------------------------------------------------------ many rows
-// Every wave of a block has its own 16 NT rows and all walk the same keys.  The
-// waves unpack a tile's codes once, each a quarter, into matrix operands in LDS
-// (two buffers, one barrier a tile); unpacking per wave would cost as much as
-// the softmax.  Two blocks share a compute unit, so that one's softmax runs
-// beside the other's matrix instructions without a common barrier.
-template <int BITS, int D, int G, int NT>
+// Every wave of a block has its own 16 NT rows and all walk the same keys, 32 SUB
+// at a time.  The waves unpack the codes once, each a quarter, into matrix
+// operands in LDS (two buffers, one barrier a step), and one wave the parameters
+// into what the softmax uses; doing either per wave would cost as much as the
+// softmax.  The block's query rows share one power of two, so that a score in
+// log2 units less the running maximum takes two multiply-adds: a key's step and
+// the row factor are one number.  Two sub-tiles a step keep matrix and vector
+// instructions of one wave independent of each other; two blocks share a
+// compute unit, so that neither waits for the other's barrier.
+template <int BITS, int D, int G>
+struct ManyTile {
+  static constexpr int kGroups = D / G;
+  f16x8 k[2][D / 32][64];
+  f16x8 v[D / 16][64];
+  f16x8 sums[64];                       // rows: zeros, steps, ones (see Wave::st)
+  float kstep[2][16][kGroups];          // key step * row factor
+  float kzero[2][16][kGroups];
+  float vstep[2][16][kGroups];          // value step * einv
+};
+template <int BITS, int D, int G, int NT, int SUB>
 struct ManyLds {
   static constexpr int kRows = kWaves * NT * 16;
-  struct Operands {
-    f16x8 k[2][D / 32][64];
-    f16x8 v[D / 16][64];
-    uint32_t param[Tile<BITS, D, G>::kParamWords];
+  struct Step {
+    ManyTile<BITS, D, G> tile[SUB];
+    float einv;
   };
+  float top[kWaves];
   union {
-    QueryRows<BITS, D, G, kRows> q;   // before the first tile
-    Operands tile[2];
+    QueryRows<BITS, D, G, kRows> q;     // before the first step
+    Step step[2];
   };
 };
 
-// A wave's quarter of a tile in registers: half s = wave / 2, part = wave % 2 of its slices and bytes.
+// A wave's quarter of a tile in registers: half s = wave / 2, part = wave % 2 of
+// its slices and bytes; the first wave also has the parameters.
 template <int BITS, int D, int G>
 struct Quarter {
   using T = Tile<BITS, D, G>;
   static constexpr int kKeyWords = T::kKeyWords / 2;          // half of a lane's share of a key row
   static constexpr int kBytes = T::kUnitBytes / 2;            // half of its share of a value row
   static constexpr int kWords = kBytes < 4 ? 1 : kBytes / 4;
-  static constexpr int kParams = (T::kGroups + kWaves - 1) / kWaves;
-  uint32_t k[kKeyWords], v[4][kWords], param[kParams];
+  uint32_t k[kKeyWords], v[4][kWords], param[T::kGroups];
   uint32_t ok;
 
   __device__ __forceinline__ void load(const KvCache& c, const Pages& pages, int hk, int tb, int wave) {
@@ -741,18 +804,17 @@ struct Quarter {
       else if constexpr (kBytes == 2) v[r][0] = *reinterpret_cast<const uint16_t*>(u);
       else load_words<kWords>(u, v[r]);
     }
+    if (wave == 0) {
 #pragma unroll
-    for (int i = 0; i < kParams; ++i) {
-      const uint32_t w = (i * kWaves + wave) * 64 + threadIdx.x % 64;
-      if (T::kGroups % kWaves && w >= T::kParamWords) continue;
-      const uint32_t run = w / (16 * T::kGroups);
-      const uint32_t* from = run & 2 ? c.v_params : c.k_params;
-      param[i] = from[(run & 1 ? row[1] : row[0]) * T::kGroups + w % (16 * T::kGroups)];
+      for (int i = 0; i < T::kGroups; ++i) {
+        const uint32_t w = i * 64 + threadIdx.x % 64, run = w / (16 * T::kGroups);
+        const uint32_t* from = run & 2 ? c.v_params : c.k_params;
+        param[i] = from[(run & 1 ? row[1] : row[0]) * T::kGroups + w % (16 * T::kGroups)];
+      }
     }
   }
 
-  template <typename Operands>
-  __device__ __forceinline__ void unpack(Operands& to, int tb, int len, int wave) const {
+  __device__ __forceinline__ void unpack(ManyTile<BITS, D, G>& to, int wave) const {
     const int lane = threadIdx.x % 64, s = wave / 2, part = wave % 2;
     constexpr int kSlices = D / 32 / 2;
 #pragma unroll
@@ -770,78 +832,310 @@ struct Quarter {
       }
       reinterpret_cast<u32x2*>(&to.v[part * kTiles + i][lane])[s] = h;
     }
+  }
+
+  // Parameters of tokens that are not there become 0: their slots may hold anything.
+  __device__ __forceinline__ void clear_missing(int tb, int len) {
 #pragma unroll
-    for (int i = 0; i < kParams; ++i) {
-      const uint32_t w = (i * kWaves + wave) * 64 + lane;
-      if (T::kGroups % kWaves && w >= T::kParamWords) continue;
-      to.param[w] = there_or_zero<T::kGroups>(param[i], w, tb, len, ok);
+    for (int i = 0; i < T::kGroups; ++i) param[i] = there_or_zero<T::kGroups>(param[i], i * 64 + threadIdx.x % 64, tb, len, ok);
+  }
+  __device__ __forceinline__ float largest_step() const {   // of this lane's values
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < T::kGroups; ++i)
+      if (i * 64 + threadIdx.x % 64 >= 32 * T::kGroups) top = fmaxf(top, f16_to_f32(param[i] & 0xffffu));
+    return top;
+  }
+  __device__ __forceinline__ void unpack_params(ManyTile<BITS, D, G>& to, float rf, float einv) const {
+#pragma unroll
+    for (int i = 0; i < T::kGroups; ++i) {
+      const int w = i * 64 + threadIdx.x % 64, at = w % (32 * T::kGroups);   // [half][token][group]
+      const float step = f16_to_f32(param[i] & 0xffffu);
+      if (w < 32 * T::kGroups) {
+        (&to.kstep[0][0][0])[at] = step * rf;
+        (&to.kzero[0][0][0])[at] = f16_to_f32(param[i] >> 16);
+      } else {
+        (&to.vstep[0][0][0])[at] = step * einv;
+        const int g = at % T::kGroups, token = at / T::kGroups, j = token / 16 * 4 + token % 4;
+        uint16_t* zeros = reinterpret_cast<uint16_t*>(&to.sums[token % 16 / 4 * 16 + g]);
+        uint16_t* steps = reinterpret_cast<uint16_t*>(&to.sums[token % 16 / 4 * 16 + T::kGroups + g]);
+        zeros[j] = (uint16_t)(param[i] >> 16);
+        steps[j] = (uint16_t)param[i];
+      }
     }
   }
 };
 
-template <int BITS, int D, int G, int NT>
+template <int BITS, int D, int G, int NT, int SUB>
 __global__ __launch_bounds__(kWaves * 64, 2) void k_kv_attention_many(KvAttnArgs a) {
-  using W = Wave<BITS, D, G, NT>;
-  using Lds = ManyLds<BITS, D, G, NT>;
+  using Lds = ManyLds<BITS, D, G, NT, SUB>;
+  using MT = ManyTile<BITS, D, G>;
+  constexpr int kSlices = D / 32, kTiles = D / 16, kGroups = D / G, kKeys = kTile * SUB;
+  constexpr float kHalf = BITS == 4 ? 8.0f : 128.0f;
+  constexpr bool kSumRow = 2 * kGroups < 16;   // see Wave
   extern __shared__ __align__(16) uint8_t shared[];
   Lds& lds = *reinterpret_cast<Lds*>(shared);
   Block k;
   if (!block_of(a, Lds::kRows, k)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int lane = threadIdx.x % 64, n = lane % 16, quad = lane / 16;
   const int first = wave * NT * 16;
-  lds.q.template stage<kWaves * 64>(a, k.sq, k.hk, k.row0, k.rows);
+
+  const float rf = lds.q.template stage_together<kWaves * 64>(a, k.sq, k.hk, k.row0, k.rows, lds.top);
   __syncthreads();
-  W w;
-  w.begin(a, k.sq, lds.q, k.row0, first, k.rows);
-  __syncthreads();   // the tiles overwrite the staged rows
+  f16x8 q[NT][kSlices];
+  float qs[NT][kGroups], mb[NT], l[NT];
+  int lo[NT], hi[NT];
+  f32x4 o[NT][kTiles], st[NT];
+  bool none[NT];               // no key seen yet
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int r = first + t * 16 + n, row = k.row0 + r;
+    const bool exists = row < k.rows;
+    const int pos = k.sq.len - k.sq.n + row / a.heads_per_kv;
+    hi[t] = !a.causal || !exists ? k.sq.len - 1 : pos < k.sq.len ? pos : k.sq.len - 1;
+    lo[t] = a.window > 0 && exists ? (int)max((int64_t)pos - a.window + 1, (int64_t)0) : 0;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) qs[t][g] = lds.q.qs[r][g] * rf;
+#pragma unroll
+    for (int w = 0; w < kSlices; ++w) q[t][w] = lds.q.op[first / 16 + t][w][lane];
+    st[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) o[t][i] = f32x4{0, 0, 0, 0};
+    mb[t] = 0.0f;
+    l[t] = 0.0f;
+    none[t] = true;
+  }
+  bool fresh = true;           // some row of the wave has seen no key yet
+  float einv = 1.0f;           // of this wave's o
+  __syncthreads();             // the steps overwrite the staged rows
+  // what no step writes: the row of ones, and rows of zeros behind it
+  for (int i = threadIdx.x; i < 2 * SUB * 64; i += kWaves * 64) {
+    const uint32_t one = kSumRow && i % 16 == 2 * kGroups ? 0x3c003c00u : 0u;
+    lds.step[i / (SUB * 64)].tile[i / 64 % SUB].sums[i % 64] = operand(one, one, one, one);
+  }
+  __syncthreads();
   // a wave without rows works along on those of the block's last row
   const Bounds r = bounds_of(a, k, min(k.row0 + first, k.rows - 1), min(k.row0 + first + NT * 16, k.rows) - 1);
   const bool idle = k.row0 + first >= k.rows;
 
-  Quarter<BITS, D, G> x;
-  uint32_t ok_now, ok_next;
+  Quarter<BITS, D, G> x[SUB];
+  float next_einv = 1.0f, limit = 0.0f;          // first wave: what the coming step's values are scaled by
+  uint32_t ok_now[SUB], ok_then[SUB];
+  auto token = [&](int t) { return k.span.token(min(t, k.t1 - 1)); };   // past the last tile: that one again
+  auto fetch = [&](int t) {
+#pragma unroll
+    for (int u = 0; u < SUB; ++u)
+      x[u].load(a.c, tile_pages(a.c, k.table, k.sq.len, token(t + u)), k.hk, token(t + u), wave);
+  };
+  auto unpack = [&](typename Lds::Step& to, int t) {
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) {
+      x[u].unpack(to.tile[u], wave);
+      ok_then[u] = x[u].ok;
+    }
+    if (wave == 0) {
+      float top = 0.0f;
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+        x[u].clear_missing(token(t + u), k.sq.len);
+        top = fmaxf(top, x[u].largest_step());
+      }
+      if (__any(top > limit)) {   // rare: products of probability and step stay in f16's range
+#pragma unroll
+        for (int i = 1; i < 64; i *= 2) top = fmaxf(top, __shfl_xor(top, i));
+        const int e = (int)(__float_as_uint(top) >> 23) - 127 + 1;   // top 2^-e in [1/2, 1)
+        next_einv = ldexpf(1.0f, -e);
+        limit = ldexpf(1.0f, e);
+      }
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) x[u].unpack_params(to.tile[u], rf, next_einv);
+      if (lane == 0) to.einv = next_einv;
+    }
+  };
   if (k.t0 < k.t1) {
-    auto token = [&](int t) { return k.span.token(min(t, k.t1 - 1)); };   // past the last tile: that one again
-    auto fetch = [&](int t) { x.load(a.c, tile_pages(a.c, k.table, k.sq.len, token(t)), k.hk, token(t), wave); };
     fetch(k.t0);
-    x.unpack(lds.tile[0], token(k.t0), k.sq.len, wave);
-    ok_now = x.ok;
-    fetch(k.t0 + 1);
+    unpack(lds.step[0], k.t0);
+    fetch(k.t0 + SUB);
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) ok_now[u] = ok_then[u];
     __syncthreads();
-    for (int t = k.t0; t < k.t1; ++t) {
-      auto& now = lds.tile[(t - k.t0) & 1];
-      auto& then = lds.tile[(t - k.t0 + 1) & 1];
-      const int tb = k.span.token(t), lane = threadIdx.x % 64;
-      if (!idle && tile_seen(r, tb, a.sinks))
-        w.step(now.param, [&](int s, int i) { return now.k[s][i][lane]; }, [&](int i) { return now.v[i][lane]; }, tb,
-               !tile_whole(r, tb, k.sq.len, ok_now, a.sinks), k.sq.len, ok_now, a.sinks);
-      x.unpack(then, token(t + 1), k.sq.len, wave);
-      ok_next = x.ok;
-      fetch(t + 2);
-      ok_now = ok_next;
+    int buffer = 0;
+    for (int t = k.t0; t < k.t1; t += SUB, buffer ^= 1) {
+      const typename Lds::Step& now = lds.step[buffer];
+      int tb[SUB];
+      bool seen = false, whole = true;
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+        tb[u] = t + u < k.t1 ? k.span.token(t + u) : 1 << 30;   // past the last tile: behind every row
+        const bool s = tile_seen(r, tb[u], a.sinks);
+        seen |= s;
+        whole &= s && tile_whole(r, tb[u], k.sq.len, ok_now[u], a.sinks);
+      }
+      if (!idle && seen) {
+        const float e = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, now.einv)));
+        if (e != einv) {
+          const float ratio = e / einv;   // powers of two
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) o[i][j] *= ratio;
+          einv = e;
+        }
+        // scores, in log2 units less the running maximum
+        float y[SUB][NT][2][4];
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+          const MT& x = now.tile[u];
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+              f32x4 acc[NT];
+#pragma unroll
+              for (int i = 0; i < NT; ++i) acc[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+              for (int w = g * G / 32; w < (g + 1) * G / 32; ++w) {
+                const f16x8 op = x.k[s][w][lane];
+#pragma unroll
+                for (int i = 0; i < NT; ++i) acc[i] = mfma(op, q[i][w], acc[i]);
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float ks = x.kstep[s][quad * 4 + j][g], kz = x.kzero[s][quad * 4 + j][g];
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                  const float z = fmaf(kz, qs[i][g], g == 0 ? -mb[i] : y[u][i][s][j]);
+                  y[u][i][s][j] = fmaf(ks, acc[i][j], z);
+                }
+              }
+            }
+          }
+        }
+        if (!whole) {
+#pragma unroll
+          for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int key = tb[u] + 16 * s + quad * 4 + j;
+                const bool there = key < k.sq.len && (ok_now[u] >> s & 1u);
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                  if (!(there && key <= hi[i] && (key >= lo[i] || key < a.sinks))) y[u][i][s][j] = -INFINITY;
+              }
+        }
+        float top[NT];
+        bool above = fresh;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          top[i] = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) top[i] = fmaxf(top[i], y[u][i][s][j]);
+          above |= top[i] > kPeak + kSlack;
+        }
+        if (__any(above)) {
+          fresh = false;
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            float m = top[i];
+            m = fmaxf(m, __shfl_xor(m, 16));
+            m = fmaxf(m, __shfl_xor(m, 32));
+            const bool any = m > -INFINITY;
+            // a row's first keys set its maximum, later ones only raise it
+            const float up = !any ? 0.0f : none[i] ? m - kPeak : fmaxf(m - kPeak, 0.0f);
+            const float alpha = none[i] ? 1.0f : __builtin_amdgcn_exp2f(-up);   // nothing to scale yet
+            mb[i] += up;
+            none[i] = none[i] && !any;
+            fresh |= none[i];
+            st[i] *= alpha;
+            l[i] *= alpha;
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) o[i][j] *= alpha;
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+              for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[u][i][s][j] -= up;
+          }
+          fresh = __any(fresh);
+        }
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+          const MT& x = now.tile[u];
+          const f16x8 sums = x.sums[lane];
+          f16x8 pv[NT][kGroups];
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            f16x8 p;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float e = __builtin_amdgcn_exp2f(y[u][i][s][j]);
+                p[4 * s + j] = (_Float16)e;
+                if constexpr (!kSumRow) l[i] += e;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) pv[i][g][4 * s + j] = (_Float16)(e * x.vstep[s][quad * 4 + j][g]);
+              }
+            st[i] = mfma(sums, p, st[i]);
+          }
+#pragma unroll
+          for (int d = 0; d < kTiles; ++d) {
+            const f16x8 op = x.v[d][lane];
+#pragma unroll
+            for (int i = 0; i < NT; ++i) o[i][d] = mfma(op, pv[i][d * 16 / G], o[i][d]);
+          }
+        }
+      }
+      unpack(lds.step[buffer ^ 1], t + SUB);
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) ok_now[u] = ok_then[u];
+      fetch(t + 2 * SUB);
       __syncthreads();
     }
   }
-  const int n = threadIdx.x % 16, quad = threadIdx.x / 16 % 4;
+  auto sum_of = [&](int i, int row) { return __shfl(st[i][row % 4], n + 16 * (row / 4)); };
+  const float up = 0x1p9f / einv;
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    const float l = w.finish(i);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const float z = fmaf(kHalf, sum_of(i, kGroups + g), sum_of(i, g));
+#pragma unroll
+      for (int d = g * G / 16; d < (g + 1) * G / 16; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][d][j] = fmaf(o[i][d][j], up, z);
+    }
+    float sum;
+    if constexpr (kSumRow) {
+      sum = sum_of(i, 2 * kGroups);
+    } else {
+      sum = l[i] + __shfl_xor(l[i], 16);
+      sum += __shfl_xor(sum, 32);
+    }
     const int row = k.row0 + first + i * 16 + n;
     if (row >= k.rows) continue;
     if (k.active <= 1) {
       const int tok = row / a.heads_per_kv, h = k.hk * a.heads_per_kv + row - tok * a.heads_per_kv;
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a row that sees nothing becomes 0
       const int64_t e = (int64_t)(k.sq.first + tok) * a.out.row_stride + (int64_t)h * a.out.head_stride + quad * 4;
 #pragma unroll
-      for (int d = 0; d < W::kTiles; ++d) store_out4(a.out, e + d * 16, w.o[i][d] * inv);
+      for (int d = 0; d < kTiles; ++d) store_out4(a.out, e + d * 16, o[i][d] * inv);
     } else {
       const int64_t at = part_index(a, k.b, k.hk, a.plan.row_blocks * Lds::kRows, row, k.split);
       if (quad == 0) {
-        a.part_ml[at * 2] = w.mb[i];
-        a.part_ml[at * 2 + 1] = l;
+        a.part_ml[at * 2] = none[i] ? kLowest : mb[i];
+        a.part_ml[at * 2 + 1] = sum;
       }
 #pragma unroll
-      for (int d = 0; d < W::kTiles; ++d) *reinterpret_cast<f32x4*>(a.part_o + at * D + d * 16 + quad * 4) = w.o[i][d];
+      for (int d = 0; d < kTiles; ++d) *reinterpret_cast<f32x4*>(a.part_o + at * D + d * 16 + quad * 4) = o[i][d];
     }
   }
 }
@@ -884,8 +1178,9 @@ hipError_t with_plan(const KvAttnArgs& a, hipStream_t st) {
     }
     return hipErrorInvalidValue;
   }
-  constexpr int NT = kv_many_tiles(D);
-  return launch_attention<kv::ManyLds<BITS, D, G, NT>>(kv::k_kv_attention_many<BITS, D, G, NT>, kv::kWaves, a, st);
+  constexpr int NT = kv_many_tiles(D), SUB = D == 256 ? 1 : 2;   // two blocks' LDS on a compute unit
+  return launch_attention<kv::ManyLds<BITS, D, G, NT, SUB>>(kv::k_kv_attention_many<BITS, D, G, NT, SUB>, kv::kWaves, a,
+                                                            st);
 }
 
 }  // namespace
