@@ -89,22 +89,26 @@ __device__ __forceinline__ void load_words(const uint8_t* __restrict__ p, uint32
   }
 }
 
-// Pages of the two halves of the tile at token tb, -1 where there is none: the
-// same in all lanes, so they are scalar loads.
+// Page of the 16 tokens at t, -1 where there is none; the same in all lanes, so
+// it is a scalar load.
+__device__ __forceinline__ int half_page(const KvCache& c, const int32_t* table, int len, int t) {
+  typedef const int32_t __attribute__((address_space(4))) * scalar_ptr;
+  int page = -1;
+  if (t < len) page = ((scalar_ptr)(uintptr_t)table)[t >> c.page_shift];
+  return page >= 0 && page < c.num_pages ? page : -1;
+}
+// The cache's row of token t in that page.  Without a page it is page 0, whose
+// memory exists; what is read there is masked.
+__device__ __forceinline__ int64_t half_row(const KvCache& c, int page, int hk, int t) {
+  return (((int64_t)(page < 0 ? 0 : page) * c.kv_heads + hk) << c.page_shift) + (t & ((1 << c.page_shift) - 1));
+}
+
+// Pages of the two halves of the tile at token tb.
 struct Pages {
   int p[2];
 };
 __device__ __forceinline__ Pages tile_pages(const KvCache& c, const int32_t* table, int len, int tb) {
-  typedef const int32_t __attribute__((address_space(4))) * scalar_ptr;
-  Pages r;
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int t = tb + 16 * s;
-    int page = -1;
-    if (t < len) page = ((scalar_ptr)(uintptr_t)table)[t >> c.page_shift];
-    r.p[s] = page >= 0 && page < c.num_pages ? page : -1;
-  }
-  return r;
+  return Pages{{half_page(c, table, len, tb), half_page(c, table, len, tb + 16)}};
 }
 
 template <int BITS, int D, int G>
@@ -118,10 +122,8 @@ __device__ __forceinline__ void load_tile(Tile<BITS, D, G>& x, const KvCache& c,
   x.ok = 0;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    // a half without a page reads page 0, whose memory exists, and is masked
-    const int64_t page = pages.p[s] < 0 ? 0 : pages.p[s];
     x.ok |= pages.p[s] < 0 ? 0u : 1u << s;
-    const int64_t row = ((page * c.kv_heads + hk) << c.page_shift) + ((tb + 16 * s) & ((1 << c.page_shift) - 1));
+    const int64_t row = half_row(c, pages.p[s], hk, tb + 16 * s);
     const uint8_t* kc = c.k_codes + row * T::kRowBytes;
     const uint8_t* vc = c.v_codes + row * T::kRowBytes;
     param[0][s] = reinterpret_cast<const uint8_t*>(c.k_params + row * T::kGroups);
@@ -738,15 +740,13 @@ __global__ __launch_bounds__(NW * 64, few_min_waves(D, NT)) void k_kv_attention_
 }
 
 // ------------------------------------------------------------------ many rows
-// Every wave of a block has its own 16 NT rows and all walk the same keys, 32 SUB
-// at a time.  The waves unpack the codes once, each a quarter, into matrix
-// operands in LDS (two buffers, one barrier a step), and one wave the parameters
-// into what the softmax uses; doing either per wave would cost as much as the
-// softmax.  The block's query rows share one power of two, so that a score in
-// log2 units less the running maximum takes two multiply-adds: a key's step and
-// the row factor are one number.  Two sub-tiles a step keep matrix and vector
-// instructions of one wave independent of each other; two blocks share a
-// compute unit, so that neither waits for the other's barrier.
+// Each of the NW waves of a block has its own 16 NT rows and all walk the same
+// keys, two tiles of 32 a step.  The waves unpack the codes once, each a quarter
+// of one tile, into matrix operands in LDS (two buffers, one barrier a step),
+// and one wave the parameters into what the softmax uses; doing either per wave
+// would cost as much as the softmax.  The block's query rows share one power of
+// two, so that a score in log2 units less the running maximum takes two
+// multiply-adds: a key's step and the row factor are one number.
 template <int BITS, int D, int G>
 struct ManyTile {
   static constexpr int kGroups = D / G;
@@ -757,43 +757,36 @@ struct ManyTile {
   float kzero[2][16][kGroups];
   float vstep[2][16][kGroups];          // value step * einv
 };
-template <int BITS, int D, int G, int NT, int SUB>
+constexpr int kSub = 2;
+template <int BITS, int D, int G, int NT, int NW>
 struct ManyLds {
-  static constexpr int kRows = kWaves * NT * 16;
+  static constexpr int kRows = NW * NT * 16;
   struct Step {
-    ManyTile<BITS, D, G> tile[SUB];
-    float einv;
+    ManyTile<BITS, D, G> tile[kSub];
+    float einv;                         // of the values' steps
+    uint32_t ok[kSub];                  // bit s: half s lies in a page of the cache
   };
-  float top[kWaves];
+  float top[NW];
   union {
     QueryRows<BITS, D, G, kRows> q;     // before the first step
     Step step[2];
   };
 };
 
-// A wave's quarter of a tile in registers: half s = wave / 2, part = wave % 2 of
-// its slices and bytes; the first wave also has the parameters.
+// A wave's quarter of a tile in registers: half s = quarter / 2, part = quarter
+// % 2 of its slices and bytes.
 template <int BITS, int D, int G>
 struct Quarter {
   using T = Tile<BITS, D, G>;
   static constexpr int kKeyWords = T::kKeyWords / 2;          // half of a lane's share of a key row
   static constexpr int kBytes = T::kUnitBytes / 2;            // half of its share of a value row
   static constexpr int kWords = kBytes < 4 ? 1 : kBytes / 4;
-  uint32_t k[kKeyWords], v[4][kWords], param[T::kGroups];
-  uint32_t ok;
+  uint32_t k[kKeyWords], v[4][kWords];
 
-  __device__ __forceinline__ void load(const KvCache& c, const Pages& pages, int hk, int tb, int wave) {
+  __device__ __forceinline__ void load(const KvCache& c, const int32_t* table, int len, int hk, int tb, int quarter) {
     const uint32_t n = threadIdx.x % 16, quad = threadIdx.x / 16 % 4;
-    const int s = wave / 2, part = wave % 2;
-    int64_t row[2];
-    ok = 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t page = pages.p[i] < 0 ? 0 : pages.p[i];   // page 0 exists; the half is masked
-      ok |= pages.p[i] < 0 ? 0u : 1u << i;
-      row[i] = ((page * c.kv_heads + hk) << c.page_shift) + ((tb + 16 * i) & ((1 << c.page_shift) - 1));
-    }
-    const int64_t mine = s ? row[1] : row[0];
+    const int s = quarter / 2, part = quarter % 2;
+    const int64_t mine = half_row(c, half_page(c, table, len, tb + 16 * s), hk, tb + 16 * s);
     const uint8_t* kc = c.k_codes + mine * T::kRowBytes + part * (kKeyWords * 4);
     const uint8_t* vc = c.v_codes + mine * T::kRowBytes + part * kBytes;
     load_words<kKeyWords>(kc + n * T::kRowBytes + quad * (T::kRowBytes / 4), k);
@@ -804,18 +797,10 @@ struct Quarter {
       else if constexpr (kBytes == 2) v[r][0] = *reinterpret_cast<const uint16_t*>(u);
       else load_words<kWords>(u, v[r]);
     }
-    if (wave == 0) {
-#pragma unroll
-      for (int i = 0; i < T::kGroups; ++i) {
-        const uint32_t w = i * 64 + threadIdx.x % 64, run = w / (16 * T::kGroups);
-        const uint32_t* from = run & 2 ? c.v_params : c.k_params;
-        param[i] = from[(run & 1 ? row[1] : row[0]) * T::kGroups + w % (16 * T::kGroups)];
-      }
-    }
   }
 
-  __device__ __forceinline__ void unpack(ManyTile<BITS, D, G>& to, int wave) const {
-    const int lane = threadIdx.x % 64, s = wave / 2, part = wave % 2;
+  __device__ __forceinline__ void unpack(ManyTile<BITS, D, G>& to, int quarter) const {
+    const int lane = threadIdx.x % 64, s = quarter / 2, part = quarter % 2;
     constexpr int kSlices = D / 32 / 2;
 #pragma unroll
     for (int w = 0; w < kSlices; ++w) to.k[s][part * kSlices + w][lane] = key_operand<BITS>(k, w);
@@ -834,6 +819,31 @@ struct Quarter {
     }
   }
 
+};
+
+// A tile's parameters in one wave's registers.
+template <int BITS, int D, int G>
+struct TileParams {
+  using T = Tile<BITS, D, G>;
+  uint32_t param[T::kGroups];
+  uint32_t ok;
+
+  __device__ __forceinline__ void load(const KvCache& c, const int32_t* table, int len, int hk, int tb) {
+    int64_t row[2];
+    ok = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int page = half_page(c, table, len, tb + 16 * i);
+      ok |= page < 0 ? 0u : 1u << i;
+      row[i] = half_row(c, page, hk, tb + 16 * i);
+    }
+#pragma unroll
+    for (int i = 0; i < T::kGroups; ++i) {
+      const uint32_t w = i * 64 + threadIdx.x % 64, run = w / (16 * T::kGroups);
+      const uint32_t* from = run & 2 ? c.v_params : c.k_params;
+      param[i] = from[(run & 1 ? row[1] : row[0]) * T::kGroups + w % (16 * T::kGroups)];
+    }
+  }
   // Parameters of tokens that are not there become 0: their slots may hold anything.
   __device__ __forceinline__ void clear_missing(int tb, int len) {
 #pragma unroll
@@ -866,11 +876,11 @@ struct Quarter {
   }
 };
 
-template <int BITS, int D, int G, int NT, int SUB>
-__global__ __launch_bounds__(kWaves * 64, 2) void k_kv_attention_many(KvAttnArgs a) {
-  using Lds = ManyLds<BITS, D, G, NT, SUB>;
+template <int BITS, int D, int G, int NT, int NW>
+__global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void k_kv_attention_many(KvAttnArgs a) {
+  using Lds = ManyLds<BITS, D, G, NT, NW>;
   using MT = ManyTile<BITS, D, G>;
-  constexpr int kSlices = D / 32, kTiles = D / 16, kGroups = D / G, kKeys = kTile * SUB;
+  constexpr int kSlices = D / 32, kTiles = D / 16, kGroups = D / G, SUB = kSub;
   constexpr float kHalf = BITS == 4 ? 8.0f : 128.0f;
   constexpr bool kSumRow = 2 * kGroups < 16;   // see Wave
   extern __shared__ __align__(16) uint8_t shared[];
@@ -881,7 +891,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_kv_attention_many(KvAttnArgs
   const int lane = threadIdx.x % 64, n = lane % 16, quad = lane / 16;
   const int first = wave * NT * 16;
 
-  const float rf = lds.q.template stage_together<kWaves * 64>(a, k.sq, k.hk, k.row0, k.rows, lds.top);
+  const float rf = lds.q.template stage_together<NW * 64>(a, k.sq, k.hk, k.row0, k.rows, lds.top);
   __syncthreads();
   f16x8 q[NT][kSlices];
   float qs[NT][kGroups], mb[NT], l[NT];
@@ -910,7 +920,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_kv_attention_many(KvAttnArgs
   float einv = 1.0f;           // of this wave's o
   __syncthreads();             // the steps overwrite the staged rows
   // what no step writes: the row of ones, and rows of zeros behind it
-  for (int i = threadIdx.x; i < 2 * SUB * 64; i += kWaves * 64) {
+  for (int i = threadIdx.x; i < 2 * SUB * 64; i += NW * 64) {
     const uint32_t one = kSumRow && i % 16 == 2 * kGroups ? 0x3c003c00u : 0u;
     lds.step[i / (SUB * 64)].tile[i / 64 % SUB].sums[i % 64] = operand(one, one, one, one);
   }
@@ -919,27 +929,32 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_kv_attention_many(KvAttnArgs
   const Bounds r = bounds_of(a, k, min(k.row0 + first, k.rows - 1), min(k.row0 + first + NT * 16, k.rows) - 1);
   const bool idle = k.row0 + first >= k.rows;
 
-  Quarter<BITS, D, G> x[SUB];
+  // Each wave fetches and unpacks its quarter of one tile (of 8 waves) or of both
+  // (of 4), the first one all parameters.
+  constexpr int kMine = SUB * 4 / NW;
+  const int quarter = wave % 4;
+  auto mine = [&](int i) { return NW == 8 ? wave / 4 : i; };
+  Quarter<BITS, D, G> codes[kMine];
+  TileParams<BITS, D, G> params[SUB];
   float next_einv = 1.0f, limit = 0.0f;          // first wave: what the coming step's values are scaled by
-  uint32_t ok_now[SUB], ok_then[SUB];
   auto token = [&](int t) { return k.span.token(min(t, k.t1 - 1)); };   // past the last tile: that one again
   auto fetch = [&](int t) {
 #pragma unroll
-    for (int u = 0; u < SUB; ++u)
-      x[u].load(a.c, tile_pages(a.c, k.table, k.sq.len, token(t + u)), k.hk, token(t + u), wave);
+    for (int i = 0; i < kMine; ++i) codes[i].load(a.c, k.table, k.sq.len, k.hk, token(t + mine(i)), quarter);
+    if (wave == 0) {
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) params[u].load(a.c, k.table, k.sq.len, k.hk, token(t + u));
+    }
   };
   auto unpack = [&](typename Lds::Step& to, int t) {
 #pragma unroll
-    for (int u = 0; u < SUB; ++u) {
-      x[u].unpack(to.tile[u], wave);
-      ok_then[u] = x[u].ok;
-    }
+    for (int i = 0; i < kMine; ++i) codes[i].unpack(to.tile[mine(i)], quarter);
     if (wave == 0) {
       float top = 0.0f;
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
-        x[u].clear_missing(token(t + u), k.sq.len);
-        top = fmaxf(top, x[u].largest_step());
+        params[u].clear_missing(token(t + u), k.sq.len);
+        top = fmaxf(top, params[u].largest_step());
       }
       if (__any(top > limit)) {   // rare: products of probability and step stay in f16's range
 #pragma unroll
@@ -949,31 +964,35 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_kv_attention_many(KvAttnArgs
         limit = ldexpf(1.0f, e);
       }
 #pragma unroll
-      for (int u = 0; u < SUB; ++u) x[u].unpack_params(to.tile[u], rf, next_einv);
-      if (lane == 0) to.einv = next_einv;
+      for (int u = 0; u < SUB; ++u) params[u].unpack_params(to.tile[u], rf, next_einv);
+      if (lane == 0) {
+        to.einv = next_einv;
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) to.ok[u] = params[u].ok;
+      }
     }
   };
   if (k.t0 < k.t1) {
     fetch(k.t0);
     unpack(lds.step[0], k.t0);
     fetch(k.t0 + SUB);
-#pragma unroll
-    for (int u = 0; u < SUB; ++u) ok_now[u] = ok_then[u];
     __syncthreads();
     int buffer = 0;
     for (int t = k.t0; t < k.t1; t += SUB, buffer ^= 1) {
       const typename Lds::Step& now = lds.step[buffer];
       int tb[SUB];
-      bool seen = false, whole = true;
+      bool seen = false;
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
         tb[u] = t + u < k.t1 ? k.span.token(t + u) : 1 << 30;   // past the last tile: behind every row
-        const bool s = tile_seen(r, tb[u], a.sinks);
-        seen |= s;
-        whole &= s && tile_whole(r, tb[u], k.sq.len, ok_now[u], a.sinks);
+        seen |= tile_seen(r, tb[u], a.sinks);
       }
       if (!idle && seen) {
-        const float e = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, now.einv)));
+        auto uniform = [](uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); };
+        const float e = __uint_as_float(uniform(__float_as_uint(now.einv)));
+        const uint32_t ok_now[SUB] = {uniform(now.ok[0]), uniform(now.ok[1])};
+        const bool whole = tile_whole(r, tb[0], k.sq.len, ok_now[0], a.sinks) &&
+                           tile_whole(r, tb[1], k.sq.len, ok_now[1], a.sinks);
         if (e != einv) {
           const float ratio = e / einv;   // powers of two
 #pragma unroll
@@ -1095,8 +1114,6 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_kv_attention_many(KvAttnArgs
         }
       }
       unpack(lds.step[buffer ^ 1], t + SUB);
-#pragma unroll
-      for (int u = 0; u < SUB; ++u) ok_now[u] = ok_then[u];
       fetch(t + 2 * SUB);
       __syncthreads();
     }
@@ -1178,9 +1195,8 @@ hipError_t with_plan(const KvAttnArgs& a, hipStream_t st) {
     }
     return hipErrorInvalidValue;
   }
-  constexpr int NT = kv_many_tiles(D), SUB = D == 256 ? 1 : 2;   // two blocks' LDS on a compute unit
-  return launch_attention<kv::ManyLds<BITS, D, G, NT, SUB>>(kv::k_kv_attention_many<BITS, D, G, NT, SUB>, kv::kWaves, a,
-                                                            st);
+  constexpr int NT = kv_many_tiles(D), NW = kv_many_waves(D);
+  return launch_attention<kv::ManyLds<BITS, D, G, NT, NW>>(kv::k_kv_attention_many<BITS, D, G, NT, NW>, NW, a, st);
 }
 
 }  // namespace

@@ -45,7 +45,7 @@ struct KvWriteArgs {
 // How an attention call is cut into blocks; a function of host arguments only.
 struct KvPlan {
   int32_t row_tiles;      // 16-row tiles a wave works on
-  int32_t row_waves;      // 1: a block's waves share its rows and take turns over the keys; 4: each has its own rows
+  int32_t row_waves;      // 1: a block's waves share its rows and take turns over the keys; more: each has its own rows
   int32_t key_waves;      // waves of a block that share rows: 4 or 8
   int32_t row_blocks;     // blocks over the rows of one (sequence, K/V head)
   int32_t splits;         // blocks over the keys
@@ -76,6 +76,7 @@ hipError_t run_kv_attention_form(const KvAttnArgs& a, hipStream_t st);
 
 // 16-row tiles of a wave where each wave has its own rows: what 256 registers hold.
 constexpr int kv_many_tiles(int head_dim) { return head_dim == 256 ? 1 : 2; }
+constexpr int kv_many_waves(int head_dim) { return head_dim == 64 ? 4 : 8; }
 KvPlan kv_attention_plan(const KvCache& c, const KvBatch& b, int heads_per_kv, int causal, int window, int sinks);
 // Rows of one (sequence, K/V head) in the partial results.
 int64_t kv_plan_rows(const KvPlan& p);

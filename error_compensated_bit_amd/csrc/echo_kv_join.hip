@@ -63,7 +63,7 @@ KvPlan kv_attention_plan(const KvCache& c, const KvBatch& b, int heads_per_kv, i
     p.row_waves = 1;
     p.row_tiles = (int32_t)((rows + 15) / 16);
   } else {
-    p.row_waves = 4;
+    p.row_waves = kv_many_waves(c.head_dim);
     p.row_tiles = kv_many_tiles(c.head_dim);
   }
   const int64_t block_rows = plan_block_rows(p);
