@@ -426,15 +426,16 @@ def echo_kv_workspace_bytes(cache: KVCache, batch: KVBatch, q_heads: int, causal
 def prepare_kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, out: torch.Tensor, scale: float,
                          causal=True, window: int = 0, sinks: int = 0, workspace: torch.Tensor | None = None,
                          stream=None) -> Prepared:
-    """workspace: uint8, at least echo_kv_workspace_bytes(); by default one of
-    the prepared call's own.  Calls that may run at the same time (other
+    """workspace: uint8, at least echo_kv_workspace_bytes(), zeros; by default one
+    of the prepared call's own.  Calls that may run at the same time (other
     streams, graphs replayed side by side) must not share one."""
     device, c, b, st = _kv_call(cache, batch, stream)
     q_heads = q.shape[1] if q.dim() == 3 else 0
     qr, outr = (_kv_rows(t, n, batch.rows, q_heads, cache.head_dim, device) for t, n in ((q, "q"), (out, "out")))
     if workspace is None:
-        workspace = torch.empty(echo_kv_workspace_bytes(cache, batch, q_heads, causal, window, sinks),
-                                dtype=torch.uint8, device=device)
+        with torch.cuda.stream(_as_stream(device, stream)):
+            workspace = torch.zeros(echo_kv_workspace_bytes(cache, batch, q_heads, causal, window, sinks),
+                                    dtype=torch.uint8, device=device)
     elif workspace.dtype != torch.uint8 or workspace.device != device:
         raise ValueError(f"workspace: uint8 on {device}")
     return _PreparedOn(load_library().echo_kv_attention,
@@ -460,7 +461,7 @@ def echo_kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, out: torc
     workspace one is allocated for this call on its stream."""
     if workspace is None:
         with torch.cuda.stream(_as_stream(cache.device, stream)):
-            workspace = torch.empty(echo_kv_workspace_bytes(cache, batch, q.shape[1], causal, window, sinks),
+            workspace = torch.zeros(echo_kv_workspace_bytes(cache, batch, q.shape[1], causal, window, sinks),
                                     dtype=torch.uint8, device=cache.device)
     prepare_kv_attention(cache, batch, q, out, scale, causal, window, sinks, workspace, stream)()
 

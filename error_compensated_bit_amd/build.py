@@ -19,7 +19,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("echo_api.hip", "echo_kernels.hip", "echo_kv_api.hip",
-                                           "echo_kv_cache.hip", "echo_kv_join.hip", "echo_kv_attention.hip")]
+                                           "echo_kv_cache.hip", "echo_kv_plan.hip", "echo_kv_attention.hip")]
 HEADERS = [os.path.join(ROOT, "include", "echo.h")] + [
     os.path.join(CSRC, f) for f in ("echo_internal.h", "echo_kv_internal.h", "echo_kv_device.h")]
 # The attention kernel is compiled once for every code width and head size.

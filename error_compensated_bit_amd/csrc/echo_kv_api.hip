@@ -12,7 +12,7 @@ using namespace echo;
 namespace {
 
 constexpr int64_t kMaxBlocks = 0xffffffffll / 256;   // a dispatch holds at most 2^32 - 1 work-items
-constexpr int64_t kMaxSeqs = 65535;                  // grid.y
+constexpr int64_t kMaxSeqs = 65535;
 constexpr int32_t kMaxRows = 1 << 30;                // row and position indices stay inside 31 bits
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -133,15 +133,18 @@ int check_attention(const echo_kv_cache* c, const echo_kv_batch* b, int q_heads,
   const KvBatch k = batch_of(b);
   if ((int64_t)k.max_new * per > (int64_t)1 << 30) return ECHO_ERR_SHAPE;
   *plan = kv_attention_plan(cache_of(c), k, per, causal, window, sinks);
-  const int64_t blocks = (int64_t)c->kv_heads * plan->row_blocks * plan->splits;
-  const int64_t joins = plan->splits > 1 ? (int64_t)c->kv_heads * kv_plan_rows(*plan) / 4 + 1 : 0;
-  if (blocks > kMaxBlocks || joins > kMaxBlocks) return ECHO_ERR_SHAPE;
+  if ((int64_t)c->kv_heads * b->seqs * plan->row_blocks > kMaxBlocks / plan->splits) return ECHO_ERR_SHAPE;
   return ECHO_OK;
 }
 
-// Outputs of every split in fp32, then their (maximum, sum) pairs.
+// Workspace of an attention call whose keys are split: kKvCounters counters,
+// the same for every call so that calls of any sizes can take turns with it,
+// the splits' outputs in fp32, and their (maximum, sum) pairs.
 int64_t part_rows(const echo_kv_cache* c, const echo_kv_batch* b, const KvPlan& p) {
   return p.splits > 1 ? (int64_t)b->seqs * c->kv_heads * kv_plan_rows(p) * p.splits : 0;
+}
+size_t workspace_bytes_of(int64_t part_rows, int head_dim) {
+  return part_rows ? ((size_t)kKvCounters + (size_t)part_rows * (head_dim + 2)) * 4 : 0;
 }
 
 int cache_rows(const echo_kv_cache* cache, const echo_kv_batch* batch, const echo_kv_rows* k, const echo_kv_rows* v,
@@ -197,7 +200,7 @@ int echo_kv_attention(const echo_kv_cache* cache, const echo_kv_batch* batch, in
   const int64_t parts = part_rows(cache, batch, a.plan);
   if (parts) {
     if ((rc = check_buf(workspace))) return rc;
-    if (workspace_bytes < (size_t)parts * (cache->head_dim + 2) * sizeof(float)) return ECHO_ERR_ARG;
+    if (workspace_bytes < workspace_bytes_of(parts, cache->head_dim)) return ECHO_ERR_ARG;
   }
   a.c = cache_of(cache);
   a.b = batch_of(batch);
@@ -210,7 +213,8 @@ int echo_kv_attention(const echo_kv_cache* cache, const echo_kv_batch* batch, in
   a.causal = causal;
   a.window = window;
   a.sinks = sinks;
-  a.part_o = static_cast<float*>(workspace);
+  a.counters = static_cast<uint32_t*>(workspace);
+  a.part_o = static_cast<float*>(workspace) + kKvCounters;
   a.part_ml = a.part_o + parts * cache->head_dim;
   return launched(run_kv_attention(a, static_cast<hipStream_t>(stream)));
 }
@@ -230,7 +234,7 @@ size_t echo_kv_workspace_bytes(const echo_kv_cache* cache, const echo_kv_batch* 
   bool empty;
   KvPlan plan;
   if (check_attention(cache, batch, q_heads, causal, window, sinks, &empty, &plan) || empty) return 0;
-  return (size_t)part_rows(cache, batch, plan) * (cache->head_dim + 2) * sizeof(float);
+  return workspace_bytes_of(part_rows(cache, batch, plan), cache->head_dim);
 }
 
 }  // extern "C"

@@ -54,11 +54,7 @@ __device__ __forceinline__ f16x8 operand(uint32_t a, uint32_t b, uint32_t c, uin
   return __builtin_bit_cast(f16x8, w);
 }
 
-// What one step loads: keys and values of 2 x 16 tokens, and their parameters
-// spread over the lanes (word 64 i + lane of [keys, values][half][token][group]).
-// Every lane needs the parameters of 8 tokens, and loading them there would take
-// 16 registers a group and buffer; they go through a few LDS words of the
-// wave's own instead.
+// How the codes of 2 x 16 tokens lie in a wave's registers.
 template <int BITS, int D, int G>
 struct Tile {
   static constexpr int kRowBytes = D * BITS / 8;
@@ -68,9 +64,6 @@ struct Tile {
   static constexpr int kGroups = D / G;
   uint32_t k[2][kKeyWords];
   uint32_t v[2][4][kUnitWords];
-  static constexpr int kParamWords = 64 * kGroups;       // of a tile
-  uint32_t param[kGroups];
-  uint32_t ok;   // bit s: the 16 tokens of half s lie in a page of the cache
 };
 
 template <int WORDS>
@@ -106,43 +99,42 @@ __device__ __forceinline__ int64_t half_row(const KvCache& c, int page, int hk, 
 // Pages of the two halves of the tile at token tb.
 struct Pages {
   int p[2];
+  __device__ __forceinline__ uint32_t ok() const { return (p[0] < 0 ? 0u : 1u) | (p[1] < 0 ? 0u : 2u); }
 };
 __device__ __forceinline__ Pages tile_pages(const KvCache& c, const int32_t* table, int len, int tb) {
-  return Pages{{half_page(c, table, len, tb), half_page(c, table, len, tb + 16)}};
+  Pages r;
+  r.p[0] = half_page(c, table, len, tb);
+  // a tile lies in one page unless pages have 16 slots
+  r.p[1] = c.page_shift == 4 ? half_page(c, table, len, tb + 16) : tb + 16 < len ? r.p[0] : -1;
+  return r;
+}
+// The cache's rows of the two halves.
+struct Halves {
+  int64_t row[2];
+};
+__device__ __forceinline__ Halves tile_halves(const KvCache& c, const Pages& pages, int hk, int tb) {
+  Halves h;
+  h.row[0] = half_row(c, pages.p[0], hk, tb);
+  h.row[1] = c.page_shift == 4 ? half_row(c, pages.p[1], hk, tb + 16) : h.row[0] + 16;
+  return h;
 }
 
 template <int BITS, int D, int G>
-__device__ __forceinline__ void load_tile(Tile<BITS, D, G>& x, const KvCache& c, const Pages& pages,
-                                          int hk, int tb) {
+__device__ __forceinline__ void load_tile(Tile<BITS, D, G>& x, const KvCache& c, const Halves& h) {
   using T = Tile<BITS, D, G>;
   const uint32_t n = threadIdx.x % 16, quad = threadIdx.x / 16 % 4;
   const uint32_t k_at = n * T::kRowBytes + quad * (T::kRowBytes / 4);
   const uint32_t v_at = quad * 4 * T::kRowBytes + n * T::kUnitBytes;
-  const uint8_t* param[2][2];
-  x.ok = 0;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    x.ok |= pages.p[s] < 0 ? 0u : 1u << s;
-    const int64_t row = half_row(c, pages.p[s], hk, tb + 16 * s);
-    const uint8_t* kc = c.k_codes + row * T::kRowBytes;
-    const uint8_t* vc = c.v_codes + row * T::kRowBytes;
-    param[0][s] = reinterpret_cast<const uint8_t*>(c.k_params + row * T::kGroups);
-    param[1][s] = reinterpret_cast<const uint8_t*>(c.v_params + row * T::kGroups);
+    const uint8_t* kc = c.k_codes + h.row[s] * T::kRowBytes;
+    const uint8_t* vc = c.v_codes + h.row[s] * T::kRowBytes;
     load_words<T::kKeyWords>(kc + k_at, x.k[s]);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       if constexpr (T::kUnitBytes == 2) x.v[s][r][0] = *reinterpret_cast<const uint16_t*>(vc + v_at + r * T::kRowBytes);
       else load_words<T::kUnitWords>(vc + v_at + r * T::kRowBytes, x.v[s][r]);
     }
-  }
-#pragma unroll
-  for (int i = 0; i < T::kGroups; ++i) {
-    const uint32_t w = i * 64 + threadIdx.x % 64;
-    const uint32_t run = w / (16 * T::kGroups);          // 0, 1: keys of each half; 2, 3: values
-    const uint8_t* lo = run & 1 ? param[0][1] : param[0][0];
-    const uint8_t* hi = run & 1 ? param[1][1] : param[1][0];
-    const uint8_t* p = run & 2 ? hi : lo;
-    x.param[i] = *reinterpret_cast<const uint32_t*>(p + w % (16 * T::kGroups) * 4);
   }
 }
 
@@ -226,13 +218,12 @@ __device__ __forceinline__ float run_reduce(float v, Op op) {
   return v;
 }
 
-// Query rows of a block in LDS: their matrix operands, and what turns a raw
-// score into log2 units.
+// Query rows of a block in LDS, as matrix operands.
 template <int BITS, int D, int G, int ROWS>
 struct QueryRows {
   static constexpr int kSlices = D / 32, kGroups = D / G, kRuns = D / 8;
   f16x8 op[ROWS / 16][kSlices][64];
-  float rf[ROWS], qs[ROWS][kGroups];
+  float qs[ROWS][kGroups];   // sums of a row's elements over a group, * 2^-24
 
   // Elements `run` of row row0 + r of a (sequence, K/V head) with `rows` rows; 0 behind the last.
   __device__ __forceinline__ u32x4 load(const KvAttnArgs& a, const Seq& sq, int hk, int row, int rows, int run) const {
@@ -271,41 +262,19 @@ struct QueryRows {
     if (run % (G / 8) == 0) qs[r][run / (G / 8)] = sum * 0x1p-24f;
   }
 
-  // Rows row0 .. row0 + ROWS - 1, each with its own power of two: the row's
-  // largest element comes into [2^14, 2^15), and bf16 values keep all their
-  // bits down to 2^-24 of the largest.
-  template <int THREADS>
-  __device__ __forceinline__ void stage(const KvAttnArgs& a, const Seq& sq, int hk, int row0, int rows) {
-    static_assert(ROWS * kRuns % 64 == 0, "whole waves");
-#pragma unroll
-    for (int pass = 0; pass * THREADS < ROWS * kRuns; ++pass) {
-      const int unit = pass * THREADS + threadIdx.x, r = unit / kRuns, run = unit % kRuns;
-      if (unit >= ROWS * kRuns) break;
-      float x[8], top = 0.0f;
-      widen(load(a, sq, hk, row0 + r, rows, run), a.q.dtype, x);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
-      top = run_reduce<kRuns>(top, [](float u, float v) { return fmaxf(u, v); });
-      const int field = (int)(__float_as_uint(top) >> 23);
-      const int up = field == 0 || field == 255 ? 0 : 14 - (field - 127);
-      put(x, up, r, run);
-      if (run == 0) rf[r] = ldexpf(a.scale_log2, 24 - up);
-    }
-  }
-
   // All rows with one power of two, from the largest finite element of the
   // block (a row 2^14 times smaller than another still keeps bf16's bits);
   // returns the factor from raw scores to log2 units.  top: a float per wave.
   template <int THREADS>
   __device__ __forceinline__ float stage_together(const KvAttnArgs& a, const Seq& sq, int hk, int row0, int rows,
                                                   float* tops) {
-    constexpr int kPasses = ROWS * kRuns / THREADS;
-    static_assert(ROWS * kRuns % THREADS == 0, "whole passes");
+    constexpr int kUnits = ROWS * kRuns, kPasses = (kUnits + THREADS - 1) / THREADS;
+    static_assert(kUnits % 64 == 0, "whole waves");
     u32x4 raw[kPasses];
 #pragma unroll
     for (int pass = 0; pass < kPasses; ++pass) {
       const int unit = pass * THREADS + threadIdx.x;
-      raw[pass] = load(a, sq, hk, row0 + unit / kRuns, rows, unit % kRuns);
+      raw[pass] = unit < kUnits ? load(a, sq, hk, row0 + unit / kRuns, rows, unit % kRuns) : u32x4{0, 0, 0, 0};
     }
     float top = 0.0f;
 #pragma unroll
@@ -327,6 +296,7 @@ struct QueryRows {
     for (int pass = 0; pass < kPasses; ++pass) {
       const int unit = pass * THREADS + threadIdx.x;
       float x[8];
+      if (unit >= kUnits) break;
       widen(raw[pass], a.q.dtype, x);
       put(x, up, unit / kRuns, unit % kRuns);
     }
@@ -334,30 +304,111 @@ struct QueryRows {
   }
 };
 
+// What the softmax of a tile of 32 keys takes of its parameters, in LDS.
+template <int D, int G>
+struct TileParams {
+  static constexpr int kGroups = D / G;
+  f16x8 sums[64];                       // operand of the sums that need no code: rows of zeros, of steps, of ones
+  float step[2][2][16][kGroups];        // key step * row factor; value step * einv
+  float kzero[2][16][kGroups];
+
+  // Eight groups leave no row of 16 for the ones.
+  static constexpr bool kSumRow = 2 * kGroups < 16;
+  // Lane `i` of what put() does not write: the row of ones, and zeros behind it.
+  __device__ __forceinline__ void clear(int i) {
+    const uint32_t one = kSumRow && i % 16 == 2 * kGroups ? 0x3c003c00u : 0u;
+    sums[i] = operand(one, one, one, one);
+  }
+};
+
+// A tile's parameter words in one wave's registers: word 64 i + lane of [keys,
+// values][half][token][group].
+template <int D, int G>
+struct ParamWords {
+  static constexpr int kGroups = D / G;
+  uint32_t word[kGroups];
+
+  __device__ __forceinline__ void load(const KvCache& c, int64_t row0, int64_t row1) {
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      const uint32_t w = i * 64 + threadIdx.x % 64, run = w / (16 * kGroups);
+      const uint32_t* from = run & 2 ? c.v_params : c.k_params;
+      word[i] = from[(run & 1 ? row1 : row0) * kGroups + w % (16 * kGroups)];
+    }
+  }
+  // Words of tokens that are not there become 0: their slots may hold anything.
+  __device__ __forceinline__ void clear_missing(int tb, int len, uint32_t ok) {
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      const int w = i * 64 + threadIdx.x % 64, s = w / (16 * kGroups) & 1, j = tb + 16 * s + w % (16 * kGroups) / kGroups;
+      if (!(j < len && (ok >> s & 1u))) word[i] = 0u;
+    }
+  }
+  __device__ __forceinline__ float largest_step() const {   // of this lane's values
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i)
+      if (i * 64 + threadIdx.x % 64 >= 32 * kGroups) top = fmaxf(top, f16_to_f32(word[i] & 0xffffu));
+    return top;
+  }
+  __device__ __forceinline__ void put(TileParams<D, G>& to, float rf, float einv) const {
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      const int w = i * 64 + threadIdx.x % 64, at = w % (32 * kGroups);   // [half][token][group]
+      const bool value = w >= 32 * kGroups;
+      (&to.step[0][0][0][0])[w] = f16_to_f32(word[i] & 0xffffu) * (value ? einv : rf);
+      if (value) {
+        const int g = at % kGroups, token = at / kGroups, j = token / 16 * 4 + token % 4;
+        uint16_t* zeros = reinterpret_cast<uint16_t*>(&to.sums[token % 16 / 4 * 16 + g]);
+        uint16_t* steps = reinterpret_cast<uint16_t*>(&to.sums[token % 16 / 4 * 16 + kGroups + g]);
+        zeros[j] = (uint16_t)(word[i] >> 16);
+        steps[j] = (uint16_t)word[i];
+      } else {
+        (&to.kzero[0][0][0])[at] = f16_to_f32(word[i] >> 16);
+      }
+    }
+  }
+};
+
+// The power of two that value steps are multiplied with, so that products of a
+// probability and a step stay in f16's range: the largest step seen comes into
+// [1/2, 1).  It changes when a larger one comes.
+struct StepScale {
+  float einv = 1.0f, limit = 0.0f;
+  // step: one of the coming values' steps per lane, all of them over the wave.
+  // True: einv has changed.
+  __device__ __forceinline__ bool see(float step) {
+    if (!__any(step > limit)) return false;
+#pragma unroll
+    for (int i = 1; i < 64; i *= 2) step = fmaxf(step, __shfl_xor(step, i));
+    const int e = (int)(__float_as_uint(step) >> 23) - 127 + 1;
+    einv = ldexpf(1.0f, -e);
+    limit = ldexpf(1.0f, e);
+    return true;
+  }
+};
+
 // The state of a wave: 16 NT query rows against the keys seen so far.
 template <int BITS, int D, int G, int NT>
 struct Wave {
+  using Params = TileParams<D, G>;
   static constexpr int kSlices = D / 32, kTiles = D / 16, kGroups = D / G;
   static constexpr float kHalf = BITS == 4 ? 8.0f : 128.0f;
-  // Rows of `st`: g: sum p zero; kGroups + g: sum p step; 2 kGroups: sum p.
-  // Eight groups leave no row for the last, which is added up in `l`.
-  static constexpr bool kSumRow = 2 * kGroups < 16;
-  f16x8 q[NT][kSlices];          // query rows as matrix operands, scaled to [2^14, 2^15)
-  float qs[NT][kGroups];         // sum of a row's q over a group, * 2^-24
-  float rf[NT];                  // raw score -> log2 units
+  f16x8 q[NT][kSlices];          // query rows as matrix operands
+  float qs[NT][kGroups];         // sum of a row's q over a group, in log2 units of score
   int lo[NT], hi[NT];            // visible keys: j <= hi and (j >= lo or j < sinks)
   f32x4 o[NT][kTiles];           // sum of p step einv (c - kHalf) 2^-9
-  f32x4 st[NT];
+  f32x4 st[NT];                  // rows: g: sum p zero; kGroups + g: sum p step; 2 kGroups: sum p
   float l[NT];                   // (!kSumRow) this lane's part of sum p
   float mb[NT];                  // running maximum (log2) - kPeak
-  float einv, elim;              // einv: a power of two with step einv <= 1 while every step <= elim
-  uint32_t psel, por;            // how this lane builds its row of the operand that gives `st`
-  int pgroup;
+  bool none[NT];                 // no key seen yet
+  bool fresh;                    // `none` of some row of the wave
+  float einv;                    // of o
 
-  // Rows row0 + first .. of the block's staged rows.
+  // Rows row0 + first .. of the block's staged rows; rf: from raw scores to log2 units.
   template <int ROWS>
   __device__ __forceinline__ void begin(const KvAttnArgs& a, const Seq& sq, const QueryRows<BITS, D, G, ROWS>& from,
-                                        int row0, int first, int rows) {
+                                        float rf, int row0, int first, int rows) {
     const int n = threadIdx.x % 16, lane = threadIdx.x % 64;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -366,180 +417,150 @@ struct Wave {
       const int pos = sq.len - sq.n + row / a.heads_per_kv;
       hi[t] = !a.causal || !exists ? sq.len - 1 : pos < sq.len ? pos : sq.len - 1;
       lo[t] = a.window > 0 && exists ? (int)max((int64_t)pos - a.window + 1, (int64_t)0) : 0;
-      rf[t] = from.rf[r];
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) qs[t][g] = from.qs[r][g];
+      for (int g = 0; g < kGroups; ++g) qs[t][g] = from.qs[r][g] * rf;
 #pragma unroll
       for (int w = 0; w < kSlices; ++w) q[t][w] = from.op[first / 16 + t][w][lane];
       st[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int i = 0; i < kTiles; ++i) o[t][i] = f32x4{0, 0, 0, 0};
-      mb[t] = kLowest;
+      mb[t] = 0.0f;
       l[t] = 0.0f;
+      none[t] = true;
     }
+    fresh = true;
     einv = 1.0f;
-    elim = 0.0f;
-    psel = n < kGroups ? 0x07060302u : n < 2 * kGroups ? 0x05040100u : 0x0c0c0c0cu;
-    por = n == 2 * kGroups ? 0x3c003c00u : 0u;
-    pgroup = n % kGroups;
   }
 
-  // One tile of 32 keys at token tb; masked: some of them some row may not see.
-  // key(s, w): operand of slice w of half s; value(i): operand of value tile i;
-  // param: the tile's parameters in LDS, 0 where there is no key; ok: as in Tile.
-  template <typename Key, typename Value>
-  __device__ __forceinline__ void step(const uint32_t* param, Key&& key, Value&& value, int tb, bool masked, int len,
-                                       uint32_t ok, int sinks) {
-    const int quad = threadIdx.x / 16 % 4;
-    // words of tokens quad * 4 + 0..3 of half s, group minor
-    auto params = [&](int array, int s, uint32_t (&w)[4][kGroups]) {
+  // o in units of another power of two.
+  __device__ __forceinline__ void set_scale(float e) {
+    if (e == einv) return;
+    const float ratio = e / einv;
 #pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(param + ((array * 2 + s) * 16 + quad * 4) * kGroups + 4 * i);
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[(4 * i + e) / kGroups][(4 * i + e) % kGroups] = v[e];
-      }
-    };
-    float sc[NT][2][4];
+      for (int i = 0; i < kTiles; ++i) o[t][i] *= ratio;
+    einv = e;
+  }
+
+  // SUB tiles of 32 keys, at tokens tb.  key(u, s, w): operand of slice w of half
+  // s of tile u; value(u, i): operand of value tile i; params(u): the tile's
+  // parameters; whole: every row sees all of the keys; ok: bit s: half s lies in
+  // a page of the cache.
+  template <int SUB, typename Key, typename Value, typename P>
+  __device__ __forceinline__ void step(Key&& key, Value&& value, P&& params, const int (&tb)[SUB], bool whole, int len,
+                                       const uint32_t (&ok)[SUB], int sinks) {
+    const int lane = threadIdx.x % 64, quad = lane / 16;
+    // scores, in log2 units less the running maximum
+    float y[SUB][NT][2][4];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      uint32_t kp[4][kGroups];
-      params(0, s, kp);
+    for (int u = 0; u < SUB; ++u) {
+      const Params& x = params(u);
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        f32x4 acc[NT];
+      for (int s = 0; s < 2; ++s) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) acc[t] = f32x4{0, 0, 0, 0};
+        for (int g = 0; g < kGroups; ++g) {
+          f32x4 acc[NT];
 #pragma unroll
-        for (int w = g * G / 32; w < (g + 1) * G / 32; ++w) {
-          const f16x8 a = key(s, w);
+          for (int i = 0; i < NT; ++i) acc[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
-          for (int t = 0; t < NT; ++t) acc[t] = mfma(a, q[t][w], acc[t]);
-        }
+          for (int w = g * G / 32; w < (g + 1) * G / 32; ++w) {
+            const f16x8 op = key(u, s, w);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float ks = f16_to_f32(kp[r][g] & 0xffffu), kz = f16_to_f32(kp[r][g] >> 16);
+            for (int i = 0; i < NT; ++i) acc[i] = mfma(op, q[i][w], acc[i]);
+          }
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const float z = g == 0 ? kz * qs[t][g] : fmaf(kz, qs[t][g], sc[t][s][r]);
-            sc[t][s][r] = fmaf(ks, acc[t][r], z);
+          for (int j = 0; j < 4; ++j) {
+            const float ks = x.step[0][s][quad * 4 + j][g], kz = x.kzero[s][quad * 4 + j][g];
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              const float z = fmaf(kz, qs[i][g], g == 0 ? -mb[i] : y[u][i][s][j]);
+              y[u][i][s][j] = fmaf(ks, acc[i][j], z);
+            }
           }
         }
       }
     }
-    if (masked) {
-      int from = tb;
-      asm volatile("" : "+s"(from));   // the comparisons stay in this branch
+    if (!whole) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int j = from + 16 * s + quad * 4 + r;
-          const bool there = j < len && (ok >> s & 1u);
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-            if (!(there && j <= hi[t] && (j >= lo[t] || j < sinks))) sc[t][s][r] = rf[t] < 0.0f ? INFINITY : -INFINITY;
-        }
-    }
-    float y[NT][2][4], vs[2][4][kGroups];
-    uint32_t vp[2][4][kGroups];
-    float top_y = -INFINITY, top_step = 0.0f;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      params(1, s, vp[s]);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          vs[s][r][g] = f16_to_f32(vp[s][r][g] & 0xffffu);
-          top_step = fmaxf(top_step, vs[s][r][g]);
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          y[t][s][r] = fmaf(sc[t][s][r], rf[t], -mb[t]);
-          top_y = fmaxf(top_y, y[t][s][r]);
-        }
-      }
-    }
-    if (__any(top_y > kPeak + kSlack || top_step > elim)) {
-      rescale(sc, top_step);
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int u = 0; u < SUB; ++u)
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) y[t][s][r] = fmaf(sc[t][s][r], rf[t], -mb[t]);
+          for (int j = 0; j < 4; ++j) {
+            const int at = tb[u] + 16 * s + quad * 4 + j;
+            const bool there = at < len && (ok[u] >> s & 1u);
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+              if (!(there && at <= hi[i] && (at >= lo[i] || at < sinks))) y[u][i][s][j] = -INFINITY;
+          }
     }
-    // the operand of the sums that need no code: zeros, steps, ones
-    uint32_t sw[2][4];
+    float top[NT];
+    bool above = fresh;
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int i = 0; i < NT; ++i) {
+      top[i] = -INFINITY;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if constexpr (kGroups == 1) sw[s][r] = vp[s][r][0];
-        else sw[s][r] = param[((2 + s) * 16 + quad * 4 + r) * kGroups + pgroup];
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) top[i] = fmaxf(top[i], y[u][i][s][j]);
+      above |= top[i] > kPeak + kSlack;
+    }
+    if (__any(above)) {
+      fresh = false;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        float m = top[i];
+        m = fmaxf(m, __shfl_xor(m, 16));
+        m = fmaxf(m, __shfl_xor(m, 32));
+        const bool any = m > -INFINITY;
+        // a row's first keys set its maximum, later ones only raise it
+        const float up = !any ? 0.0f : none[i] ? m - kPeak : fmaxf(m - kPeak, 0.0f);
+        const float alpha = none[i] ? 1.0f : __builtin_amdgcn_exp2f(-up);   // nothing to scale yet
+        mb[i] += up;
+        none[i] = none[i] && !any;
+        fresh |= none[i];
+        st[i] *= alpha;
+        l[i] *= alpha;
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) o[i][j] *= alpha;
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[u][i][s][j] -= up;
       }
-    auto pick = [&](int s, int r) { return __builtin_amdgcn_perm(sw[s][r + 1], sw[s][r], psel) | por; };
-    const f16x8 sums = operand(pick(0, 0), pick(0, 2), pick(1, 0), pick(1, 2));
-    f16x8 pv[NT][kGroups];
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) vs[s][r][g] *= einv;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      f16x8 p;
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float e = __builtin_amdgcn_exp2f(y[t][s][r]);
-          p[4 * s + r] = (_Float16)e;
-          if constexpr (!kSumRow) l[t] += e;
-#pragma unroll
-          for (int g = 0; g < kGroups; ++g) pv[t][g][4 * s + r] = (_Float16)(e * vs[s][r][g]);
-        }
-      st[t] = mfma(sums, p, st[t]);
+      fresh = __any(fresh);
     }
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      const f16x8 a = value(i);
+    for (int u = 0; u < SUB; ++u) {
+      const Params& x = params(u);
+      const f16x8 sums = x.sums[lane];
+      f16x8 pv[NT][kGroups];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) o[t][i] = mfma(a, pv[t][i * 16 / G], o[t][i]);
-    }
-  }
-
-  // Raise the running maxima to the largest scores and the normaliser to the largest step.
-  __device__ __forceinline__ void rescale(const float (&sc)[NT][2][4], float top_step) {
-    top_step = fmaxf(top_step, __shfl_xor(top_step, 16));
-    top_step = fmaxf(top_step, __shfl_xor(top_step, 32));
-    float ratio = 1.0f;
-    if (top_step > elim) {      // the same in the whole wave
-      const int e = (int)(__float_as_uint(top_step) >> 23) - 127 + 1;   // top_step 2^-e in [1/2, 1)
-      const float inv = ldexpf(1.0f, -e);
-      ratio = elim > 0.0f ? inv / einv : 1.0f;   // powers of two
-      einv = inv;
-      elim = ldexpf(1.0f, e);
-    }
+      for (int i = 0; i < NT; ++i) {
+        f16x8 p;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float top = mb[t] + kPeak;
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+          for (int j = 0; j < 4; ++j) {
+            const float e = __builtin_amdgcn_exp2f(y[u][i][s][j]);
+            p[4 * s + j] = (_Float16)e;
+            if constexpr (!Params::kSumRow) l[i] += e;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) top = fmaxf(top, sc[t][s][r] * rf[t]);
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      top -= kPeak;
-      const float alpha = __builtin_amdgcn_exp2f(mb[t] - top);
-      mb[t] = top;
-      st[t] *= alpha;
-      l[t] *= alpha;
-      const float both = alpha * ratio;
+            for (int g = 0; g < kGroups; ++g) pv[i][g][4 * s + j] = (_Float16)(e * x.step[1][s][quad * 4 + j][g]);
+          }
+        st[i] = mfma(sums, p, st[i]);
+      }
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) o[t][i] *= both;
+      for (int d = 0; d < kTiles; ++d) {
+        const f16x8 op = value(u, d);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) o[i][d] = mfma(op, pv[i][d * 16 / G], o[i][d]);
+      }
     }
   }
 
@@ -547,6 +568,9 @@ struct Wave {
   __device__ __forceinline__ float sum_of(int t, int row) const {
     return __shfl(st[t][row % 4], (int)(threadIdx.x % 16) + 16 * (row / 4));
   }
+
+  // The running maximum of tile t's rows as the join takes it.
+  __device__ __forceinline__ float maximum(int t) const { return none[t] ? kLowest : mb[t]; }
 
   // The sum of probabilities of tile t's rows; the outputs in the same units, in place of o.
   __device__ __forceinline__ float finish(int t) {
@@ -559,7 +583,7 @@ struct Wave {
 #pragma unroll
         for (int r = 0; r < 4; ++r) o[t][i][r] = fmaf(o[t][i][r], up, z);
     }
-    if constexpr (kSumRow) return sum_of(t, 2 * kGroups);
+    if constexpr (Params::kSumRow) return sum_of(t, 2 * kGroups);
     float sum = l[t] + __shfl_xor(l[t], 16);
     return sum + __shfl_xor(sum, 32);
   }
@@ -570,24 +594,27 @@ struct Wave {
 struct Block {
   Seq sq;
   Span span;
-  int b, hk, split, row0, rows, active, t0, t1;
+  int b, hk, rb, split, row0, rows, active, t0, t1;
   const int32_t* table;
 };
 struct Bounds {
   int hi_min, hi_max, lo_min, lo_max;
 };
 
-// grid.x: K/V head fastest, then split, then block of rows (the last rows
-// first: under a causal mask they have the most keys); grid.y: sequence.
+// grid.x: K/V head fastest, then sequence, block of rows (the last rows first:
+// under a causal mask they have the most keys), split: long blocks start early.
 // False: the block has nothing to do.
 __device__ __forceinline__ bool block_of(const KvAttnArgs& a, int block_rows, Block& k) {
-  k.b = blockIdx.y;
-  k.hk = blockIdx.x % a.c.kv_heads;
-  const int rest = blockIdx.x / a.c.kv_heads;
-  k.split = rest % a.plan.splits;
+  uint32_t id = blockIdx.x;
+  k.hk = (int)(id % (uint32_t)a.c.kv_heads);
+  id /= (uint32_t)a.c.kv_heads;
+  k.b = (int)(id % (uint32_t)a.b.seqs);
+  id /= (uint32_t)a.b.seqs;
+  k.rb = a.plan.row_blocks - 1 - (int)(id % (uint32_t)a.plan.row_blocks);
+  k.split = (int)(id / (uint32_t)a.plan.row_blocks);
   k.sq = sequence(a, k.b);
   k.rows = k.sq.computed * a.heads_per_kv;
-  k.row0 = (a.plan.row_blocks - 1 - rest / a.plan.splits) * block_rows;
+  k.row0 = k.rb * block_rows;
   if (k.row0 >= k.rows) return false;
   const int last = min(k.row0 + block_rows, k.rows) - 1;
   k.span = key_span(a, k.sq.len, k.sq.n, k.row0 / a.heads_per_kv, last / a.heads_per_kv);
@@ -609,13 +636,6 @@ __device__ __forceinline__ bool tile_whole(const Bounds& r, int tb, int len, uin
   return tb + kTile - 1 <= r.hi_min && tb + kTile <= len && ok == 3u && (tb >= r.lo_max || tb + kTile <= sinks);
 }
 
-// A word of the tile's parameters, 0 for a token that is not there (its slot may hold anything).
-template <int GROUPS>
-__device__ __forceinline__ uint32_t there_or_zero(uint32_t word, int w, int tb, int len, uint32_t ok) {
-  const int s = w / (16 * GROUPS) & 1, j = tb + 16 * s + w % (16 * GROUPS) / GROUPS;
-  return j < len && (ok >> s & 1u) ? word : 0u;
-}
-
 __device__ __forceinline__ void store_out8(const KvRows& out, int64_t e, const float* v) {
   u32x4 w;
   if (out.dtype == kKvF16) {
@@ -628,6 +648,57 @@ __device__ __forceinline__ void store_out8(const KvRows& out, int64_t e, const f
   *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out.p) + e) = w;
 }
 
+// The splits' results pass between blocks on different dies, whose L2 caches are
+// not coherent: they are stored and loaded as agent-scope atomics, which go
+// through to the common memory.  (Fences of that scope write back and drop the
+// whole L2 instead: with one per block a decode step of 64 sequences took 150
+// us in place of 46.)
+__device__ __forceinline__ void put_shared(float* p, float v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float get_shared(const float* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Behind the stores of a split's results: the last of the splits of a block's
+// rows to arrive joins them all, in the order of the splits.  It leaves the
+// counter 0 for the next call.  `word`: LDS.
+template <int D, int THREADS>
+__device__ __forceinline__ void join_splits(const KvAttnArgs& a, const Block& k, int block_rows, uint32_t* word) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's results have arrived
+  __syncthreads();                                    // and the other waves'
+  if (threadIdx.x == 0) {
+    uint32_t* counter = a.counters + ((int64_t)k.b * a.c.kv_heads + k.hk) * a.plan.row_blocks + k.rb;
+    *word = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (*word == (uint32_t)k.active - 1) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (*word != (uint32_t)k.active - 1) return;
+  constexpr int kRuns = D / 8;
+  const int rows = min(block_rows, k.rows - k.row0);
+  for (int unit = threadIdx.x; unit < rows * kRuns; unit += THREADS) {
+    const int row = k.row0 + unit / kRuns, run = unit % kRuns;
+    const int64_t at = part_index(a, k.b, k.hk, a.plan.row_blocks * block_rows, row, 0);
+    const float* ml = a.part_ml + at * 2;
+    const float* po = a.part_o + at * D + run * 8;
+    float top = kLowest, sum = 0.0f, v[8] = {};
+#pragma unroll 4
+    for (int s = 0; s < k.active; ++s) top = fmaxf(top, get_shared(ml + 2 * s));
+#pragma unroll 4
+    for (int s = 0; s < k.active; ++s) {
+      const float f = __builtin_amdgcn_exp2f(get_shared(ml + 2 * s) - top);
+      sum = fmaf(get_shared(ml + 2 * s + 1), f, sum);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = fmaf(get_shared(po + (int64_t)s * D + e), f, v[e]);
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int i = row / a.heads_per_kv, h = k.hk * a.heads_per_kv + row - i * a.heads_per_kv;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= inv;
+    store_out8(a.out, (int64_t)(k.sq.first + i) * a.out.row_stride + (int64_t)h * a.out.head_stride + run * 8, v);
+  }
+}
+
 // ------------------------------------------------------------------ few rows
 // The NW waves of a block share its 16 NT rows and take turns over the keys:
 // wave w has the tiles w, w + NW, ...  Loads go to registers, the next tile's
@@ -637,18 +708,22 @@ template <int BITS, int D, int G, int NT, int NW>
 struct FewLds {
   static constexpr int kRows = NT * 16, kStride = D + 4;
   QueryRows<BITS, D, G, kRows> q;
-  uint32_t param[NW][Tile<BITS, D, G>::kParamWords];
+  float top[NW];
   float m[NW][kRows], l[NW][kRows];
-  float o[NW][kRows][kStride];
+  union {
+    TileParams<D, G> params;    // in the wave's loop
+    float o[kRows][kStride];    // behind it
+  } wave[NW];
 };
 
-// Waves per SIMD that the registers have to leave room for.
-constexpr int few_min_waves(int D, int NT) {
-  return NT == 1 ? (D == 64 ? 4 : D == 128 ? 3 : 2) : NT == 2 && D <= 128 ? 2 : 1;
+// Waves per SIMD that the registers leave room for without spilling.
+constexpr int few_min_waves(int BITS, int D, int G, int NT) {
+  if (NT == 1) return D == 64 ? (BITS * (64 / G) > 8 ? 3 : 4) : D == 128 ? (BITS == 4 && G > 32 ? 3 : 2) : BITS == 4 && G > 32 ? 2 : 1;
+  return BITS * (128 / G) < 32 ? 2 : 1;
 }
 
 template <int BITS, int D, int G, int NT, int NW>
-__global__ __launch_bounds__(NW * 64, few_min_waves(D, NT)) void k_kv_attention_few(KvAttnArgs a) {
+__global__ __launch_bounds__(NW * 64, few_min_waves(BITS, D, G, NT)) void k_kv_attention_few(KvAttnArgs a) {
   using W = Wave<BITS, D, G, NT>;
   using Lds = FewLds<BITS, D, G, NT, NW>;
   extern __shared__ __align__(16) uint8_t shared[];
@@ -658,50 +733,65 @@ __global__ __launch_bounds__(NW * 64, few_min_waves(D, NT)) void k_kv_attention_
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   int t = k.t0 + wave;
   Tile<BITS, D, G> x, y;
-  Pages next = {{-1, -1}};
-  // a load past the last tile repeats it; nothing uses the copy
-  auto fetch = [&](Tile<BITS, D, G>& into, int at) {
-    load_tile(into, a.c, next, k.hk, k.span.token(min(at, k.t1 - 1)));
-    next = tile_pages(a.c, k.table, k.sq.len, k.span.token(min(at + NW, k.t1 - 1)));
+  ParamWords<D, G> x_words, y_words;
+  uint32_t x_ok = 0, y_ok = 0;
+  // past the last tile the loads repeat it; nothing uses the copy
+  auto token = [&](int at) { return k.span.token(min(at, k.t1 - 1)); };
+  Pages pages = {{-1, -1}};   // of the next tile to load
+  auto fetch = [&](Tile<BITS, D, G>& into, ParamWords<D, G>& words, uint32_t& ok, int at) {
+    const Halves h = tile_halves(a.c, pages, k.hk, token(at));
+    ok = pages.ok();
+    load_tile(into, a.c, h);
+    words.load(a.c, h.row[0], h.row[1]);
+    pages = tile_pages(a.c, k.table, k.sq.len, token(at + NW));
   };
   if (t < k.t1) {
-    next = tile_pages(a.c, k.table, k.sq.len, k.span.token(t));
-    fetch(x, t);
+    pages = tile_pages(a.c, k.table, k.sq.len, token(t));
+    fetch(x, x_words, x_ok, t);
   }
-  lds.q.template stage<NW * 64>(a, k.sq, k.hk, k.row0, k.rows);
+  TileParams<D, G>& params = lds.wave[wave].params;
+  params.clear(threadIdx.x % 64);
+  const float rf = lds.q.template stage_together<NW * 64>(a, k.sq, k.hk, k.row0, k.rows, lds.top);
   __syncthreads();
   W w;
-  w.begin(a, k.sq, lds.q, k.row0, 0, k.rows);
+  w.begin(a, k.sq, lds.q, rf, k.row0, 0, k.rows);
+  StepScale scale;
   const Bounds r = bounds_of(a, k, k.row0, min(k.row0 + Lds::kRows, k.rows) - 1);
-  uint32_t* param = lds.param[wave];
-  for (; t < k.t1; t += NW) {
-    fetch(y, t + NW);
-    const int tb = k.span.token(t);
-    if (tile_seen(r, tb, a.sinks)) {
-      const bool whole = tile_whole(r, tb, k.sq.len, x.ok, a.sinks);
+  auto work = [&](const Tile<BITS, D, G>& from, ParamWords<D, G>& words, uint32_t page_ok) {
+    const int tb[1] = {k.span.token(t)};
+    if (tile_seen(r, tb[0], a.sinks)) {
+      const uint32_t ok[1] = {page_ok};
+      const bool whole = tile_whole(r, tb[0], k.sq.len, page_ok, a.sinks);
+      if (!whole) words.clear_missing(tb[0], k.sq.len, page_ok);
+      if (scale.see(words.largest_step())) w.set_scale(scale.einv);
       wave_sync();
-#pragma unroll
-      for (int i = 0; i < W::kGroups; ++i) {
-        const int at = i * 64 + threadIdx.x % 64;
-        param[at] = whole ? x.param[i] : there_or_zero<W::kGroups>(x.param[i], at, tb, k.sq.len, x.ok);
-      }
+      words.put(params, rf, scale.einv);
       wave_sync();
-      w.step(param, [&](int s, int i) { return key_operand<BITS>(x.k[s], i); },
-             [&](int i) { return value_operand<BITS>(x.v, i); }, tb, !whole, k.sq.len, x.ok, a.sinks);
+      w.template step<1>([&](int, int s, int i) { return key_operand<BITS>(from.k[s], i); },
+                         [&](int, int i) { return value_operand<BITS>(from.v, i); },
+                         [&](int) -> const TileParams<D, G>& { return params; }, tb, whole, k.sq.len, ok, a.sinks);
     }
-    x = y;
+    t += NW;
+  };
+  while (t < k.t1) {   // two buffers taking turns: a copy would wait for the loads in flight
+    fetch(y, y_words, y_ok, t + NW);
+    work(x, x_words, x_ok);
+    if (t >= k.t1) break;
+    fetch(x, x_words, x_ok, t + NW);
+    work(y, y_words, y_ok);
   }
   const int n = threadIdx.x % 16, quad = threadIdx.x / 16 % 4;
+  wave_sync();
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     const float l = w.finish(i);
     const int row = i * 16 + n;
     if (quad == 0) {
-      lds.m[wave][row] = w.mb[i];
+      lds.m[wave][row] = w.maximum(i);
       lds.l[wave][row] = l;
     }
 #pragma unroll
-    for (int e = 0; e < W::kTiles; ++e) *reinterpret_cast<f32x4*>(&lds.o[wave][row][e * 16 + quad * 4]) = w.o[i][e];
+    for (int e = 0; e < W::kTiles; ++e) *reinterpret_cast<f32x4*>(&lds.wave[wave].o[row][e * 16 + quad * 4]) = w.o[i][e];
   }
   __syncthreads();
   constexpr int kRuns = D / 8;
@@ -718,7 +808,7 @@ __global__ __launch_bounds__(NW * 64, few_min_waves(D, NT)) void k_kv_attention_
       const float f = __builtin_amdgcn_exp2f(lds.m[i][r0] - top);
       sum = fmaf(lds.l[i][r0], f, sum);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = fmaf(lds.o[i][r0][run * 8 + e], f, v[e]);
+      for (int e = 0; e < 8; ++e) v[e] = fmaf(lds.wave[i].o[r0][run * 8 + e], f, v[e]);
     }
     if (k.active <= 1) {
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a row that sees nothing becomes 0
@@ -729,14 +819,14 @@ __global__ __launch_bounds__(NW * 64, few_min_waves(D, NT)) void k_kv_attention_
     } else {
       const int64_t at = part_index(a, k.b, k.hk, a.plan.row_blocks * Lds::kRows, row, k.split);
       if (run == 0) {
-        a.part_ml[at * 2] = top;
-        a.part_ml[at * 2 + 1] = sum;
+        put_shared(a.part_ml + at * 2, top);
+        put_shared(a.part_ml + at * 2 + 1, sum);
       }
-      f32x4* to = reinterpret_cast<f32x4*>(a.part_o + at * D + run * 8);
-      to[0] = f32x4{v[0], v[1], v[2], v[3]};
-      to[1] = f32x4{v[4], v[5], v[6], v[7]};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) put_shared(a.part_o + at * D + run * 8 + e, v[e]);
     }
   }
+  if (k.active > 1) join_splits<D, NW * 64>(a, k, Lds::kRows, reinterpret_cast<uint32_t*>(lds.top));
 }
 
 // ------------------------------------------------------------------ many rows
@@ -749,13 +839,9 @@ __global__ __launch_bounds__(NW * 64, few_min_waves(D, NT)) void k_kv_attention_
 // multiply-adds: a key's step and the row factor are one number.
 template <int BITS, int D, int G>
 struct ManyTile {
-  static constexpr int kGroups = D / G;
   f16x8 k[2][D / 32][64];
   f16x8 v[D / 16][64];
-  f16x8 sums[64];                       // rows: zeros, steps, ones (see Wave::st)
-  float kstep[2][16][kGroups];          // key step * row factor
-  float kzero[2][16][kGroups];
-  float vstep[2][16][kGroups];          // value step * einv
+  TileParams<D, G> params;
 };
 constexpr int kSub = 2;
 template <int BITS, int D, int G, int NT, int NW>
@@ -821,68 +907,11 @@ struct Quarter {
 
 };
 
-// A tile's parameters in one wave's registers.
-template <int BITS, int D, int G>
-struct TileParams {
-  using T = Tile<BITS, D, G>;
-  uint32_t param[T::kGroups];
-  uint32_t ok;
-
-  __device__ __forceinline__ void load(const KvCache& c, const int32_t* table, int len, int hk, int tb) {
-    int64_t row[2];
-    ok = 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int page = half_page(c, table, len, tb + 16 * i);
-      ok |= page < 0 ? 0u : 1u << i;
-      row[i] = half_row(c, page, hk, tb + 16 * i);
-    }
-#pragma unroll
-    for (int i = 0; i < T::kGroups; ++i) {
-      const uint32_t w = i * 64 + threadIdx.x % 64, run = w / (16 * T::kGroups);
-      const uint32_t* from = run & 2 ? c.v_params : c.k_params;
-      param[i] = from[(run & 1 ? row[1] : row[0]) * T::kGroups + w % (16 * T::kGroups)];
-    }
-  }
-  // Parameters of tokens that are not there become 0: their slots may hold anything.
-  __device__ __forceinline__ void clear_missing(int tb, int len) {
-#pragma unroll
-    for (int i = 0; i < T::kGroups; ++i) param[i] = there_or_zero<T::kGroups>(param[i], i * 64 + threadIdx.x % 64, tb, len, ok);
-  }
-  __device__ __forceinline__ float largest_step() const {   // of this lane's values
-    float top = 0.0f;
-#pragma unroll
-    for (int i = 0; i < T::kGroups; ++i)
-      if (i * 64 + threadIdx.x % 64 >= 32 * T::kGroups) top = fmaxf(top, f16_to_f32(param[i] & 0xffffu));
-    return top;
-  }
-  __device__ __forceinline__ void unpack_params(ManyTile<BITS, D, G>& to, float rf, float einv) const {
-#pragma unroll
-    for (int i = 0; i < T::kGroups; ++i) {
-      const int w = i * 64 + threadIdx.x % 64, at = w % (32 * T::kGroups);   // [half][token][group]
-      const float step = f16_to_f32(param[i] & 0xffffu);
-      if (w < 32 * T::kGroups) {
-        (&to.kstep[0][0][0])[at] = step * rf;
-        (&to.kzero[0][0][0])[at] = f16_to_f32(param[i] >> 16);
-      } else {
-        (&to.vstep[0][0][0])[at] = step * einv;
-        const int g = at % T::kGroups, token = at / T::kGroups, j = token / 16 * 4 + token % 4;
-        uint16_t* zeros = reinterpret_cast<uint16_t*>(&to.sums[token % 16 / 4 * 16 + g]);
-        uint16_t* steps = reinterpret_cast<uint16_t*>(&to.sums[token % 16 / 4 * 16 + T::kGroups + g]);
-        zeros[j] = (uint16_t)(param[i] >> 16);
-        steps[j] = (uint16_t)param[i];
-      }
-    }
-  }
-};
-
 template <int BITS, int D, int G, int NT, int NW>
 __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void k_kv_attention_many(KvAttnArgs a) {
   using Lds = ManyLds<BITS, D, G, NT, NW>;
-  using MT = ManyTile<BITS, D, G>;
-  constexpr int kSlices = D / 32, kTiles = D / 16, kGroups = D / G, SUB = kSub;
-  constexpr float kHalf = BITS == 4 ? 8.0f : 128.0f;
-  constexpr bool kSumRow = 2 * kGroups < 16;   // see Wave
+  using W = Wave<BITS, D, G, NT>;
+  constexpr int SUB = kSub;
   extern __shared__ __align__(16) uint8_t shared[];
   Lds& lds = *reinterpret_cast<Lds*>(shared);
   Block k;
@@ -893,37 +922,11 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void k_kv_attention_many(
 
   const float rf = lds.q.template stage_together<NW * 64>(a, k.sq, k.hk, k.row0, k.rows, lds.top);
   __syncthreads();
-  f16x8 q[NT][kSlices];
-  float qs[NT][kGroups], mb[NT], l[NT];
-  int lo[NT], hi[NT];
-  f32x4 o[NT][kTiles], st[NT];
-  bool none[NT];               // no key seen yet
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int r = first + t * 16 + n, row = k.row0 + r;
-    const bool exists = row < k.rows;
-    const int pos = k.sq.len - k.sq.n + row / a.heads_per_kv;
-    hi[t] = !a.causal || !exists ? k.sq.len - 1 : pos < k.sq.len ? pos : k.sq.len - 1;
-    lo[t] = a.window > 0 && exists ? (int)max((int64_t)pos - a.window + 1, (int64_t)0) : 0;
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) qs[t][g] = lds.q.qs[r][g] * rf;
-#pragma unroll
-    for (int w = 0; w < kSlices; ++w) q[t][w] = lds.q.op[first / 16 + t][w][lane];
-    st[t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i) o[t][i] = f32x4{0, 0, 0, 0};
-    mb[t] = 0.0f;
-    l[t] = 0.0f;
-    none[t] = true;
-  }
-  bool fresh = true;           // some row of the wave has seen no key yet
-  float einv = 1.0f;           // of this wave's o
+  W w;
+  w.begin(a, k.sq, lds.q, rf, k.row0, first, k.rows);
   __syncthreads();             // the steps overwrite the staged rows
-  // what no step writes: the row of ones, and rows of zeros behind it
-  for (int i = threadIdx.x; i < 2 * SUB * 64; i += NW * 64) {
-    const uint32_t one = kSumRow && i % 16 == 2 * kGroups ? 0x3c003c00u : 0u;
-    lds.step[i / (SUB * 64)].tile[i / 64 % SUB].sums[i % 64] = operand(one, one, one, one);
-  }
+  for (int i = threadIdx.x; i < 2 * SUB * 64; i += NW * 64)
+    lds.step[i / (SUB * 64)].tile[i / 64 % SUB].params.clear(i % 64);
   __syncthreads();
   // a wave without rows works along on those of the block's last row
   const Bounds r = bounds_of(a, k, min(k.row0 + first, k.rows - 1), min(k.row0 + first + NT * 16, k.rows) - 1);
@@ -935,15 +938,21 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void k_kv_attention_many(
   const int quarter = wave % 4;
   auto mine = [&](int i) { return NW == 8 ? wave / 4 : i; };
   Quarter<BITS, D, G> codes[kMine];
-  TileParams<BITS, D, G> params[SUB];
-  float next_einv = 1.0f, limit = 0.0f;          // first wave: what the coming step's values are scaled by
+  ParamWords<D, G> words[SUB];
+  uint32_t ok[SUB];
+  StepScale scale;                               // first wave: of the coming step's values
   auto token = [&](int t) { return k.span.token(min(t, k.t1 - 1)); };   // past the last tile: that one again
   auto fetch = [&](int t) {
 #pragma unroll
     for (int i = 0; i < kMine; ++i) codes[i].load(a.c, k.table, k.sq.len, k.hk, token(t + mine(i)), quarter);
     if (wave == 0) {
 #pragma unroll
-      for (int u = 0; u < SUB; ++u) params[u].load(a.c, k.table, k.sq.len, k.hk, token(t + u));
+      for (int u = 0; u < SUB; ++u) {
+        const Pages pages = tile_pages(a.c, k.table, k.sq.len, token(t + u));
+        const Halves h = tile_halves(a.c, pages, k.hk, token(t + u));
+        words[u].load(a.c, h.row[0], h.row[1]);
+        ok[u] = pages.ok();
+      }
     }
   };
   auto unpack = [&](typename Lds::Step& to, int t) {
@@ -953,22 +962,16 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void k_kv_attention_many(
       float top = 0.0f;
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
-        params[u].clear_missing(token(t + u), k.sq.len);
-        top = fmaxf(top, params[u].largest_step());
+        words[u].clear_missing(token(t + u), k.sq.len, ok[u]);
+        top = fmaxf(top, words[u].largest_step());
       }
-      if (__any(top > limit)) {   // rare: products of probability and step stay in f16's range
+      scale.see(top);
 #pragma unroll
-        for (int i = 1; i < 64; i *= 2) top = fmaxf(top, __shfl_xor(top, i));
-        const int e = (int)(__float_as_uint(top) >> 23) - 127 + 1;   // top 2^-e in [1/2, 1)
-        next_einv = ldexpf(1.0f, -e);
-        limit = ldexpf(1.0f, e);
-      }
-#pragma unroll
-      for (int u = 0; u < SUB; ++u) params[u].unpack_params(to.tile[u], rf, next_einv);
+      for (int u = 0; u < SUB; ++u) words[u].put(to.tile[u].params, rf, scale.einv);
       if (lane == 0) {
-        to.einv = next_einv;
+        to.einv = scale.einv;
 #pragma unroll
-        for (int u = 0; u < SUB; ++u) to.ok[u] = params[u].ok;
+        for (int u = 0; u < SUB; ++u) to.ok[u] = ok[u];
       }
     }
   };
@@ -989,154 +992,23 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void k_kv_attention_many(
       }
       if (!idle && seen) {
         auto uniform = [](uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); };
-        const float e = __uint_as_float(uniform(__float_as_uint(now.einv)));
+        w.set_scale(__uint_as_float(uniform(__float_as_uint(now.einv))));
         const uint32_t ok_now[SUB] = {uniform(now.ok[0]), uniform(now.ok[1])};
         const bool whole = tile_whole(r, tb[0], k.sq.len, ok_now[0], a.sinks) &&
                            tile_whole(r, tb[1], k.sq.len, ok_now[1], a.sinks);
-        if (e != einv) {
-          const float ratio = e / einv;   // powers of two
-#pragma unroll
-          for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int j = 0; j < kTiles; ++j) o[i][j] *= ratio;
-          einv = e;
-        }
-        // scores, in log2 units less the running maximum
-        float y[SUB][NT][2][4];
-#pragma unroll
-        for (int u = 0; u < SUB; ++u) {
-          const MT& x = now.tile[u];
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-              f32x4 acc[NT];
-#pragma unroll
-              for (int i = 0; i < NT; ++i) acc[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-              for (int w = g * G / 32; w < (g + 1) * G / 32; ++w) {
-                const f16x8 op = x.k[s][w][lane];
-#pragma unroll
-                for (int i = 0; i < NT; ++i) acc[i] = mfma(op, q[i][w], acc[i]);
-              }
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float ks = x.kstep[s][quad * 4 + j][g], kz = x.kzero[s][quad * 4 + j][g];
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                  const float z = fmaf(kz, qs[i][g], g == 0 ? -mb[i] : y[u][i][s][j]);
-                  y[u][i][s][j] = fmaf(ks, acc[i][j], z);
-                }
-              }
-            }
-          }
-        }
-        if (!whole) {
-#pragma unroll
-          for (int u = 0; u < SUB; ++u)
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int key = tb[u] + 16 * s + quad * 4 + j;
-                const bool there = key < k.sq.len && (ok_now[u] >> s & 1u);
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-                  if (!(there && key <= hi[i] && (key >= lo[i] || key < a.sinks))) y[u][i][s][j] = -INFINITY;
-              }
-        }
-        float top[NT];
-        bool above = fresh;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          top[i] = -INFINITY;
-#pragma unroll
-          for (int u = 0; u < SUB; ++u)
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) top[i] = fmaxf(top[i], y[u][i][s][j]);
-          above |= top[i] > kPeak + kSlack;
-        }
-        if (__any(above)) {
-          fresh = false;
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            float m = top[i];
-            m = fmaxf(m, __shfl_xor(m, 16));
-            m = fmaxf(m, __shfl_xor(m, 32));
-            const bool any = m > -INFINITY;
-            // a row's first keys set its maximum, later ones only raise it
-            const float up = !any ? 0.0f : none[i] ? m - kPeak : fmaxf(m - kPeak, 0.0f);
-            const float alpha = none[i] ? 1.0f : __builtin_amdgcn_exp2f(-up);   // nothing to scale yet
-            mb[i] += up;
-            none[i] = none[i] && !any;
-            fresh |= none[i];
-            st[i] *= alpha;
-            l[i] *= alpha;
-#pragma unroll
-            for (int j = 0; j < kTiles; ++j) o[i][j] *= alpha;
-#pragma unroll
-            for (int u = 0; u < SUB; ++u)
-#pragma unroll
-              for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) y[u][i][s][j] -= up;
-          }
-          fresh = __any(fresh);
-        }
-#pragma unroll
-        for (int u = 0; u < SUB; ++u) {
-          const MT& x = now.tile[u];
-          const f16x8 sums = x.sums[lane];
-          f16x8 pv[NT][kGroups];
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            f16x8 p;
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float e = __builtin_amdgcn_exp2f(y[u][i][s][j]);
-                p[4 * s + j] = (_Float16)e;
-                if constexpr (!kSumRow) l[i] += e;
-#pragma unroll
-                for (int g = 0; g < kGroups; ++g) pv[i][g][4 * s + j] = (_Float16)(e * x.vstep[s][quad * 4 + j][g]);
-              }
-            st[i] = mfma(sums, p, st[i]);
-          }
-#pragma unroll
-          for (int d = 0; d < kTiles; ++d) {
-            const f16x8 op = x.v[d][lane];
-#pragma unroll
-            for (int i = 0; i < NT; ++i) o[i][d] = mfma(op, pv[i][d * 16 / G], o[i][d]);
-          }
-        }
+        w.template step<SUB>([&](int u, int s, int i) { return now.tile[u].k[s][i][lane]; },
+                             [&](int u, int i) { return now.tile[u].v[i][lane]; },
+                             [&](int u) -> const TileParams<D, G>& { return now.tile[u].params; }, tb, whole, k.sq.len,
+                             ok_now, a.sinks);
       }
       unpack(lds.step[buffer ^ 1], t + SUB);
       fetch(t + 2 * SUB);
       __syncthreads();
     }
   }
-  auto sum_of = [&](int i, int row) { return __shfl(st[i][row % 4], n + 16 * (row / 4)); };
-  const float up = 0x1p9f / einv;
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      const float z = fmaf(kHalf, sum_of(i, kGroups + g), sum_of(i, g));
-#pragma unroll
-      for (int d = g * G / 16; d < (g + 1) * G / 16; ++d)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][d][j] = fmaf(o[i][d][j], up, z);
-    }
-    float sum;
-    if constexpr (kSumRow) {
-      sum = sum_of(i, 2 * kGroups);
-    } else {
-      sum = l[i] + __shfl_xor(l[i], 16);
-      sum += __shfl_xor(sum, 32);
-    }
+    const float sum = w.finish(i);
     const int row = k.row0 + first + i * 16 + n;
     if (row >= k.rows) continue;
     if (k.active <= 1) {
@@ -1144,17 +1016,20 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void k_kv_attention_many(
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a row that sees nothing becomes 0
       const int64_t e = (int64_t)(k.sq.first + tok) * a.out.row_stride + (int64_t)h * a.out.head_stride + quad * 4;
 #pragma unroll
-      for (int d = 0; d < kTiles; ++d) store_out4(a.out, e + d * 16, o[i][d] * inv);
+      for (int d = 0; d < W::kTiles; ++d) store_out4(a.out, e + d * 16, w.o[i][d] * inv);
     } else {
       const int64_t at = part_index(a, k.b, k.hk, a.plan.row_blocks * Lds::kRows, row, k.split);
       if (quad == 0) {
-        a.part_ml[at * 2] = none[i] ? kLowest : mb[i];
-        a.part_ml[at * 2 + 1] = sum;
+        put_shared(a.part_ml + at * 2, w.maximum(i));
+        put_shared(a.part_ml + at * 2 + 1, sum);
       }
 #pragma unroll
-      for (int d = 0; d < kTiles; ++d) *reinterpret_cast<f32x4*>(a.part_o + at * D + d * 16 + quad * 4) = o[i][d];
+      for (int d = 0; d < W::kTiles; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) put_shared(a.part_o + at * D + d * 16 + quad * 4 + j, w.o[i][d][j]);
     }
   }
+  if (k.active > 1) join_splits<D, NW * 64>(a, k, Lds::kRows, reinterpret_cast<uint32_t*>(lds.top));
 }
 
 }  // namespace kv
@@ -1166,7 +1041,7 @@ using IC = std::integral_constant<int, V>;
 
 template <typename Lds>
 hipError_t launch_attention(void (*kernel)(KvAttnArgs), int waves, const KvAttnArgs& a, hipStream_t st) {
-  const unsigned blocks = (unsigned)((int64_t)a.c.kv_heads * a.plan.row_blocks * a.plan.splits);
+  const unsigned blocks = (unsigned)((int64_t)a.c.kv_heads * a.b.seqs * a.plan.row_blocks * a.plan.splits);
   static_assert(sizeof(Lds) <= 160 * 1024, "LDS of a compute unit");
   if (sizeof(Lds) > 64 * 1024) {   // more than a launch gives without asking
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
@@ -1175,7 +1050,7 @@ hipError_t launch_attention(void (*kernel)(KvAttnArgs), int waves, const KvAttnA
   }
   KvAttnArgs args = a;
   void* ptrs[] = {&args};
-  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(blocks, a.b.seqs), dim3(waves * 64), ptrs,
+  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(blocks), dim3(waves * 64), ptrs,
                          sizeof(Lds), st);
 }
 
@@ -1187,13 +1062,10 @@ hipError_t with_plan(const KvAttnArgs& a, hipStream_t st) {
     return launch_attention<kv::FewLds<BITS, D, G, NT(), NW()>>(kv::k_kv_attention_few<BITS, D, G, NT(), NW()>, NW(), a, st);
   };
   if (p.row_waves == 1) {
-    if (p.row_tiles == 1 && p.key_waves == 4) return few(IC<1>{}, IC<4>{});
-    if (p.row_tiles == 1) return few(IC<1>{}, IC<8>{});
-    if (p.row_tiles == 2) return few(IC<2>{}, IC<4>{});
     if constexpr (D <= 128) {
-      if (p.row_tiles == 3) return few(IC<3>{}, IC<4>{});
+      if (p.row_tiles == 2) return few(IC<2>{}, IC<4>{});
     }
-    return hipErrorInvalidValue;
+    return p.key_waves == 8 ? few(IC<1>{}, IC<8>{}) : few(IC<1>{}, IC<4>{});
   }
   constexpr int NT = kv_many_tiles(D), NW = kv_many_waves(D);
   return launch_attention<kv::ManyLds<BITS, D, G, NT, NW>>(kv::k_kv_attention_many<BITS, D, G, NT, NW>, NW, a, st);

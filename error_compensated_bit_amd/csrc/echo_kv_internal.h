@@ -42,6 +42,9 @@ struct KvWriteArgs {
   KvRows k, v;
 };
 
+// Arrival counters in a workspace: keys are split only where there are fewer blocks of rows than this.
+constexpr int kKvCounters = 256;
+
 // How an attention call is cut into blocks; a function of host arguments only.
 struct KvPlan {
   int32_t row_tiles;      // 16-row tiles a wave works on
@@ -60,7 +63,8 @@ struct KvAttnArgs {
   float scale_log2;       // softmax scale * log2(e)
   int32_t causal, window, sinks;
   KvPlan plan;
-  float *part_o, *part_ml;   // partial results of the splits; see echo_kv_attention.hip
+  uint32_t* counters;        // arrived splits of every (sequence, K/V head, block of rows); 0 between calls
+  float *part_o, *part_ml;   // results of the splits: [seq][K/V head][row][split] of D floats, and (maximum, sum)
 };
 
 // Each returns the first launch error (hipSuccess when every launch went out).

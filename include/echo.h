@@ -281,8 +281,11 @@ int echo_kv_read(const echo_kv_cache* cache, const echo_kv_batch* batch,
  *   Scores, the softmax and sums are binary32 on the unrounded cached values;
  *   probabilities enter the second product in fp16, relative to the row's
  *   maximum.
- *   workspace: echo_kv_workspace_bytes() bytes (may be NULL if that is 0), not
- *   used by another call at the same time; its contents do not matter.
+ *   workspace: echo_kv_workspace_bytes() bytes (may be NULL if that is 0), all 0
+ *   when it is first used, and again after a call that failed with
+ *   ECHO_ERR_HIP; a completed call leaves it ready for the next, of any sizes
+ *   that fit.  Calls that may run at the same time (on other streams, in graphs
+ *   replayed side by side) must not share one.
  *   Errors: ECHO_ERR_ARG (also a workspace too small), ECHO_ERR_SHAPE,
  *   ECHO_ERR_ALIGN, ECHO_ERR_HIP.
  */
