@@ -3,7 +3,8 @@
 The payload a rank sends to an owner is a device buffer the owner's pass reads
 directly, which stands in for the all-to-all; the owners' requantized payloads
 are read the same way by the dequantize pass, which stands in for the
-all-gather.  Only the library's entry points run; nothing here computes.
+all-gather.  Only the library's entry points run, and attention_site()'s
+output projection (a plain matrix product); nothing else here computes.
 """
 from __future__ import annotations
 
@@ -84,3 +85,42 @@ def share(cfg, r: Ranks, rank: int, x: torch.Tensor, stream=None):
     entry(cfg, r, rank, x, stream)
     owner(cfg, r, rank, x, stream)
     gather(cfg, r, stream)
+
+
+@dataclass
+class AttentionRanks:
+    """A tensor-parallel attention site over P ranks: rank p holds its K/V
+    heads' cache, the rows of the output projection that belong to its query
+    heads, and the buffers of its part of a call."""
+    caches: list               # caches[p]: rank p's K/V heads
+    projections: list          # projections[p]: [query heads * head_dim, hidden]
+    workspace: torch.Tensor    # one for all ranks, whose calls follow each other
+    attended: list             # attended[p]: [rows, query heads, head_dim]
+    partial: list              # partial[p]: [rows, hidden], rank p's message
+
+
+def alloc_attention(P: int, num_pages: int, page_size: int, kv_heads: int, head_dim: int, projections,
+                    batches, bits: int = 4, group: int = B.ECHO_GROUP, device="cuda") -> AttentionRanks:
+    """kv_heads: of one rank.  batches: one KVBatch of every size of call (their
+    rows, max_new and max_len size the buffers)."""
+    caches = [B.alloc_kv_cache(num_pages, page_size, kv_heads, head_dim, bits, group, device) for _ in range(P)]
+    q_heads, hidden = projections[0].shape[0] // head_dim, projections[0].shape[1]
+    dt, rows = projections[0].dtype, max(b.rows for b in batches)
+    room = max(B.echo_kv_workspace_bytes(caches[0], b, q_heads) for b in batches)
+    return AttentionRanks(caches, list(projections), torch.zeros(room, dtype=torch.uint8, device=device),
+                          [torch.empty(rows, q_heads, head_dim, dtype=dt, device=device) for _ in range(P)],
+                          [torch.empty(rows, hidden, dtype=dt, device=device) for _ in range(P)])
+
+
+def attention_site(cfg, r: Ranks, a: AttentionRanks, batch: B.KVBatch, qs, ks, vs, scale: float) -> torch.Tensor:
+    """One attention site on the current stream: every rank writes its heads'
+    new keys and values, attends over its cache and multiplies with its rows of
+    the output projection; the partial products are summed by one call.
+    qs, ks, vs: the ranks' projected rows [batch.rows, heads, head_dim];
+    r: ranks with messages of batch.rows * hidden elements."""
+    for p in range(r.P):
+        att, part = a.attended[p][:batch.rows], a.partial[p][:batch.rows]
+        B.echo_kv_write(a.caches[p], batch, ks[p], vs[p])
+        B.echo_kv_attention(a.caches[p], batch, qs[p], att, scale, workspace=a.workspace)
+        torch.mm(att.flatten(1), a.projections[p], out=part)
+    return allreduce(cfg, r, [a.partial[p][:batch.rows].reshape(-1) for p in range(r.P)])
