@@ -312,3 +312,55 @@ def test_two_graphs_with_their_own_workspaces():
         torch.cuda.synchronize()
         for o in outs:
             assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("seqs,per,new,D,bits,group", [
+    (270, 4, 1, 128, 4, 128), (270, 8, 1, 64, 8, 32), (270, 3, 1, 256, 8, 64),     # one tile of rows, 4 waves
+    (140, 6, 4, 128, 4, 64), (20, 6, 4, 128, 4, 64),                               # 24 rows, many and few pairs
+    (140, 5, 8, 256, 4, 128), (140, 7, 8, 256, 8, 32), (20, 10, 10, 256, 4, 64),   # 256 elements, 40, 56 and 100 rows
+    (140, 13, 8, 64, 4, 64), (140, 13, 8, 128, 8, 128), (5, 43, 3, 64, 8, 64),     # 104 and 129 rows
+])
+def test_forms_chosen_by_pairs_and_rows(seqs, per, new, D, bits, group):
+    """Sizes on both sides of every choice of kernel form, with sequences of very
+    different lengths in one call."""
+    lens = np.random.default_rng(seqs + per).integers(1, 45, seqs).tolist()
+    lens[seqs // 2] = 333
+    Case(lens, [min(new, n) for n in lens], heads=1, per=per, D=D, bits=bits, group=group, seed=30).run_and_check()
+
+
+@pytest.mark.parametrize("D,new", [(64, 300), (128, 300), (256, 150)])
+def test_many_rows_split_and_joined(D, new):
+    c = Case([4200, 170], [new, 60], heads=1, per=1, D=D, group=64, page=64, seed=31)
+    assert B.echo_kv_workspace_bytes(c.cache, c.batch(), 1) > 0
+    c.run_and_check()
+
+
+def test_one_workspace_for_calls_that_follow_each_other():
+    """A workspace of the largest call serves smaller ones in between; a call
+    leaves its counters at 0; one that is too small is refused."""
+    cases = [Case([4000, 700], [3, 1], heads=1, per=4, seed=32), Case([2500], [1], heads=2, per=2, D=64, group=64, seed=33),
+             Case([1500, 3, 1200], [40, 3, 40], heads=1, per=8, seed=34)]
+    sizes = [B.echo_kv_workspace_bytes(c.cache, c.batch(), c.heads * c.per) for c in cases]
+    assert min(sizes) > 0 and len(set(sizes)) == 3
+    want = [c.run() for c in cases]
+    work = torch.zeros(max(sizes), dtype=torch.uint8, device=DEV)
+    for i in (0, 1, 2, 1, 0, 2):
+        c = cases[i]
+        q = c.q.to(DEV)
+        out = torch.zeros_like(q)
+        B.echo_kv_attention(c.cache, c.batch(), q, out, c.scale, workspace=work)
+        assert torch.equal(out, want[i])
+        assert not work[:1024].any()
+        with pytest.raises(B.EchoError):
+            B.echo_kv_attention(c.cache, c.batch(), q, out, c.scale, workspace=work[:sizes[i] - 4])
+
+
+def test_empty_calls_and_sequences():
+    """No sequences, no rows, sequences without rows or without keys: nothing but the given rows is written."""
+    c = Case([50, 0, 7, 20], [4, 0, 0, 1], seed=35)
+    c.run_and_check()
+    q = torch.zeros(0, 8, 128, dtype=torch.bfloat16, device=DEV)
+    none = B.KVBatch(torch.zeros(1, dtype=torch.int32, device=DEV), torch.zeros(0, dtype=torch.int32, device=DEV),
+                     torch.zeros(0, 4, dtype=torch.int32, device=DEV), 0, 0, 0)
+    B.echo_kv_attention(c.cache, none, q, torch.empty_like(q), 0.1)
+    torch.cuda.synchronize()

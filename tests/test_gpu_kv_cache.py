@@ -262,3 +262,34 @@ def test_offsets_past_32_bits():
         w = np.exp(s - s.max())
         want = w @ values[1][:, h] / w.sum()
         assert np.abs(U.host64(o[i, h]) - want).max() < 0.01 * np.abs(want).max() + 2 ** -9 * np.abs(want).max()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_every_step(bits):
+    """Every fp16 step: groups whose range is that step's, its midpoint to the
+    next and the binary32 neighbours of the midpoint, with elements on and next to
+    the codes' midpoints, where a quotient or reciprocal off by one bit shows."""
+    top = float(2 ** bits - 1)
+    steps = np.arange(0x7C00, dtype=np.uint16).view(np.float16).astype(np.float64)
+    mid = np.float32((steps + np.append(steps[1:], 65536.0)) / 2 * top)
+    low, high = np.nextafter(mid, np.float32(0)), np.nextafter(mid, np.float32(np.inf))
+    x = np.zeros((4, len(steps), 64), np.float32)
+    x[:, :, 1] = np.stack([np.float32(steps * top), low, mid, high])
+    codes = np.arange(20) if bits == 4 else np.r_[0:7, 120:127, 249:255]
+    codes = codes[codes < top]
+    ties = (codes + 0.5) * steps[:, None]
+    for i, t in enumerate((ties.astype(np.float32), np.nextafter(np.float32(ties), np.float32(0)),
+                           np.nextafter(np.float32(ties), np.float32(np.inf)))):
+        at = 2 + i * len(codes)
+        x[:, :, at:at + len(codes)] = np.fmin(t, x[:, :, 1:2])
+    rows = x.reshape(-1, 1, 64)
+    lay = U.Layout([len(rows)], [len(rows)], 256)
+    cache = make_cache(lay, 1, 64, bits, 64)
+    k = torch.from_numpy(rows).to(DEV)
+    B.echo_kv_write(cache, lay.batch(), k, k)
+    torch.cuda.synchronize()
+    pages, slots = lay.slots(0, range(len(rows)))
+    want = U.quantize(rows.astype(np.float64), bits, 64)
+    for stored in U.cache_rows(cache):
+        for have, w in zip(stored, want):
+            np.testing.assert_array_equal(have[pages, 0, slots], w[:, 0])
