@@ -388,6 +388,12 @@ struct StepScale {
   }
 };
 
+// How far the many-row step's LDS reads are ahead of their use.
+enum class Ahead { kNothing, kOperands, kAll };
+constexpr Ahead ahead(int D, int G) {
+  return D == 128 && G == 128 ? Ahead::kAll : D / G <= (D == 64 ? 1 : 2) ? Ahead::kOperands : Ahead::kNothing;
+}
+
 // The state of a wave: 16 NT query rows against the keys seen so far.
 template <int BITS, int D, int G, int NT>
 struct Wave {
@@ -451,36 +457,62 @@ struct Wave {
   __device__ __forceinline__ void step(Key&& key, Value&& value, P&& params, const int (&tb)[SUB], bool whole, int len,
                                        const uint32_t (&ok)[SUB], int sinks) {
     const int lane = threadIdx.x % 64, quad = lane / 16;
-    // scores, in log2 units less the running maximum
+    // scores, in log2 units less the running maximum; half h % 2 of tile h / 2
     float y[SUB][NT][2][4];
+    constexpr int kHalves = 2 * SUB;
+    constexpr Ahead kAhead = SUB > 1 ? ahead(D, G) : Ahead::kNothing;
+    f16x8 ops[2][kSlices];
+    f32x4 acc[2][kGroups][NT];
+    float ks[2][kGroups][4], kz[2][kGroups][4];
+    auto keys = [&](int h) {
 #pragma unroll
-    for (int u = 0; u < SUB; ++u) {
-      const Params& x = params(u);
+      for (int w = 0; w < kSlices; ++w) ops[h % 2][w] = key(h / 2, h % 2, w);
+    };
+    auto factors = [&](int h, int g) {
+      const Params& x = params(h / 2);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
+      for (int j = 0; j < 4; ++j) {
+        ks[h % 2][g][j] = x.step[0][h % 2][quad * 4 + j][g];
+        kz[h % 2][g][j] = x.kzero[h % 2][quad * 4 + j][g];
+      }
+    };
+    auto scores = [&](int h, int g) {
+      if constexpr (kAhead != Ahead::kAll) factors(h, g);
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          f32x4 acc[NT];
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int i = 0; i < NT; ++i) acc[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-          for (int w = g * G / 32; w < (g + 1) * G / 32; ++w) {
-            const f16x8 op = key(u, s, w);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) acc[i] = mfma(op, q[i][w], acc[i]);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float ks = x.step[0][s][quad * 4 + j][g], kz = x.kzero[s][quad * 4 + j][g];
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              const float z = fmaf(kz, qs[i][g], g == 0 ? -mb[i] : y[u][i][s][j]);
-              y[u][i][s][j] = fmaf(ks, acc[i][j], z);
-            }
-          }
+        for (int i = 0; i < NT; ++i) {
+          const float z = fmaf(kz[h % 2][g][j], qs[i][g], g == 0 ? -mb[i] : y[h / 2][i][h % 2][j]);
+          y[h / 2][i][h % 2][j] = fmaf(ks[h % 2][g][j], acc[h % 2][g][i][j], z);
         }
+    };
+    if constexpr (kAhead != Ahead::kNothing) keys(0);
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+      if constexpr (kAhead != Ahead::kNothing) {
+        if constexpr (kAhead == Ahead::kAll)
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) factors(h, g);
+        if (h + 1 < kHalves) keys(h + 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) acc[h % 2][g][i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int w = g * G / 32; w < (g + 1) * G / 32; ++w) {
+          const f16x8 op = kAhead != Ahead::kNothing ? ops[h % 2][w] : key(h / 2, h % 2, w);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) acc[h % 2][g][i] = mfma(op, q[i][w], acc[h % 2][g][i]);
+        }
+        if constexpr (kAhead == Ahead::kNothing) scores(h, g);
+        else if (h > 0) scores(h - 1, g);
       }
     }
+    if constexpr (kAhead != Ahead::kNothing)
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) scores(kHalves - 1, g);
     if (!whole) {
 #pragma unroll
       for (int u = 0; u < SUB; ++u)
@@ -535,6 +567,13 @@ struct Wave {
       }
       fresh = __any(fresh);
     }
+    constexpr int kDeep = D == 64 ? 2 : 4;
+    f16x8 vops[kDeep];
+    if constexpr (kAhead != Ahead::kNothing) {
+#pragma unroll
+      for (int d = 0; d < kDeep; ++d) vops[d] = value(0, d);
+      __builtin_amdgcn_sched_barrier(0);
+    }
 #pragma unroll
     for (int u = 0; u < SUB; ++u) {
       const Params& x = params(u);
@@ -555,11 +594,23 @@ struct Wave {
           }
         st[i] = mfma(sums, p, st[i]);
       }
+      if constexpr (kAhead == Ahead::kNothing) {
 #pragma unroll
-      for (int d = 0; d < kTiles; ++d) {
-        const f16x8 op = value(u, d);
+        for (int d = 0; d < kTiles; ++d) {
+          const f16x8 op = value(u, d);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) o[i][d] = mfma(op, pv[i][d * 16 / G], o[i][d]);
+          for (int i = 0; i < NT; ++i) o[i][d] = mfma(op, pv[i][d * 16 / G], o[i][d]);
+        }
+      } else {
+#pragma unroll
+        for (int d = 0; d < kTiles; ++d) {
+          const f16x8 op = vops[d % kDeep];
+          if (d + kDeep < kTiles) vops[d % kDeep] = value(u, d + kDeep);
+          else if (u + 1 < SUB) vops[d % kDeep] = value(u + 1, d + kDeep - kTiles);
+          __builtin_amdgcn_sched_barrier(0x406);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) o[i][d] = mfma(op, pv[i][d * 16 / G], o[i][d]);
+        }
       }
     }
   }
