@@ -1116,7 +1116,10 @@ hipError_t with_plan(const KvAttnArgs& a, hipStream_t st) {
     if constexpr (D <= 128) {
       if (p.row_tiles == 2) return few(IC<2>{}, IC<4>{});
     }
-    return p.key_waves == 8 ? few(IC<1>{}, IC<8>{}) : few(IC<1>{}, IC<4>{});
+    if constexpr (BITS * D <= 1024) {
+      if (p.key_waves == 8) return few(IC<1>{}, IC<8>{});
+    }
+    return few(IC<1>{}, IC<4>{});
   }
   constexpr int NT = kv_many_tiles(D), NW = kv_many_waves(D);
   return launch_attention<kv::ManyLds<BITS, D, G, NT, NW>>(kv::k_kv_attention_many<BITS, D, G, NT, NW>, NW, a, st);
