@@ -20,15 +20,22 @@
 // rows per 16x16x32 instruction: its result gives lane (n = lane % 16, quad =
 // lane / 16) the keys 4 quad + 0..3 of query row n, which is, for two such
 // tiles, exactly the operand that O^T = V^T P^T wants from that lane.  So
-// probabilities never leave their lane, and keys, values and parameters go
-// from global memory to registers in the order the cache stores them
-// (echo_kv_device.h): no LDS and no barrier in the loop.
+// probabilities never leave their lane.  The cache stores keys and values in
+// the order in which lanes take them (echo_kv_device.h).
 //
-// A wave works on NT tiles of 16 query rows (row = new token x query head of
-// one K/V head) and walks 32 keys at a time, the next tile's loads in flight
-// during the current one's arithmetic.  The running maximum moves only when a
-// score exceeds it by more than 2^4, which keeps the rescaling of the output
-// out of almost every step.
+// A wave works on NT tiles of 16 query rows (row = new token x query head of one
+// K/V head) and walks the keys 32 or 64 at a time.  The running maximum moves
+// only when a score exceeds it by more than 2^4, which keeps the rescaling of
+// the output out of almost every step.  Two kernels: for few rows, where the
+// cache's bytes bound the time, codes go from memory to registers; for many,
+// where the arithmetic does, a block unpacks them once into LDS.  Where there
+// are fewer blocks than compute units, the keys are split too and the last
+// block to arrive joins the parts.
+//
+// Measured (bf16, 4 bits in groups of 128, 32 query and 8 K/V heads of 128
+// elements): one new token of 4 sequences of about 126000 keys 106 us, 5.2 TB/s;
+// of 64 sequences of 1000 to 7000 keys 45 us, 4.1 TB/s (the longest sequence's
+// block is the whole time); 2048 new tokens after 16384 670 us, 870 TFLOP/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -61,7 +68,6 @@ struct Tile {
   static constexpr int kKeyWords = kRowBytes / 16;       // words of a lane's share of one key row
   static constexpr int kUnitBytes = kRowBytes / 16;      // bytes of a lane's share of one value row
   static constexpr int kUnitWords = kUnitBytes < 4 ? 1 : kUnitBytes / 4;
-  static constexpr int kGroups = D / G;
   uint32_t k[2][kKeyWords];
   uint32_t v[2][4][kUnitWords];
 };
@@ -388,7 +394,12 @@ struct StepScale {
   }
 };
 
-// How far the many-row step's LDS reads are ahead of their use.
+// What the many-row step reads from LDS ahead of its use: left to itself the
+// compiler puts each read right before its two matrix instructions, and the
+// wave waits for it (2048 rows after 16384 keys of 128 elements: 743 us, with
+// operands ahead 674, parameters too 665; where that spills it costs more: 64
+// elements 334 us without parameters, 430 with).  kOperands: matrix operands;
+// kAll: a half's parameters too.
 enum class Ahead { kNothing, kOperands, kAll };
 constexpr Ahead ahead(int D, int G) {
   return D == 128 && G == 128 ? Ahead::kAll : D / G <= (D == 64 ? 1 : 2) ? Ahead::kOperands : Ahead::kNothing;
@@ -1114,7 +1125,7 @@ hipError_t with_plan(const KvAttnArgs& a, hipStream_t st) {
   };
   if (p.row_waves == 1) {
     if constexpr (D <= 128) {
-      if (p.row_tiles == 2) return few(IC<2>{}, IC<4>{});
+      if (p.row_tiles == 2) return p.key_waves == 8 ? few(IC<2>{}, IC<8>{}) : few(IC<2>{}, IC<4>{});
     }
     if constexpr (BITS * D <= 1024) {
       if (p.key_waves == 8) return few(IC<1>{}, IC<8>{});

@@ -83,6 +83,11 @@ __device__ __forceinline__ void store8(void* p, int64_t e, const float* v) {
   }
 }
 
+struct QParams {
+  float zf, sf, inv;
+  uint32_t word;  // step bits | zero bits << 16
+};
+
 // Group parameters: the all-reduce quantizer's, without the compiler's full
 // divisions, which cost a fifth of the kernel's instructions.  span / qmax
 // is the product with the rounded reciprocal and one correction, which rounds

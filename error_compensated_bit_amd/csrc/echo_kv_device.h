@@ -38,11 +38,6 @@ __device__ __forceinline__ uint32_t f32_to_bf16(float f) {
   return __builtin_bit_cast(uint16_t, (__bf16)f);
 }
 
-struct QParams {
-  float zf, sf, inv;
-  uint32_t word;  // step bits | zero bits << 16
-};
-
 // A sequence and its entries of the batch's arrays; seq < 0: none.
 struct SeqEntry {
   int seq, start, end, len;
@@ -89,9 +84,8 @@ __host__ __device__ __forceinline__ int64_t row_place(const KvCache& c, const Kv
   return ((page * c.kv_heads) << c.page_shift) + (pos & ((1 << c.page_shift) - 1));
 }
 
-// ---- shared by the attention kernel and the one that joins its splits
-constexpr int kTile = 32;            // keys per step
-constexpr int kWaves = 4;            // waves per block
+// ---- attention
+constexpr int kTile = 32;            // keys per tile
 constexpr float kLowest = -3.0e38f;  // running maximum before any key: below every finite score
 
 // The keys a block's rows can see, as tiles: those below `t1` start at 0, the

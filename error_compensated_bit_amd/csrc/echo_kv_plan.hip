@@ -30,9 +30,10 @@ KvPlan kv_attention_plan(const KvCache& c, const KvBatch& b, int heads_per_kv, i
   p.key_waves = 4;
   if (rows <= few) {
     p.row_waves = 1;
-    // two tiles of rows a wave share the unpacking, one leaves more waves: 24
-    // rows, 512 pairs 70 / 49 us (one / two), 128 pairs 27 / 35 us; with 256
-    // elements two do not fit the registers of two waves a SIMD
+    // two tiles of rows a wave share the unpacking, one gives twice the blocks
+    // and half the rows to join: 24 rows, 512 pairs 70 / 49 us (one / two), 128
+    // pairs 26 / 30 us, 8 pairs of 32768 keys 36 / 64 us; with 256 elements two
+    // do not fit the registers of two waves a SIMD
     p.row_tiles = rows <= 16 || c.head_dim == 256 || (rows <= 32 && thin) ? 1 : 2;
   } else {
     p.row_waves = kv_many_waves(c.head_dim);
@@ -55,10 +56,11 @@ KvPlan kv_attention_plan(const KvCache& c, const KvBatch& b, int heads_per_kv, i
   if (splits > tiles / 16) splits = tiles / 16;
   if (splits < 1 || blocks > kKvCounters) splits = 1;
   const int64_t per = (tiles + splits - 1) / splits;
-  // with a block or less for a compute unit, 8 waves a block take half the steps
-  // (one sequence of 32768 keys: 23 us, with 4 waves 27); 256 elements of 8 bits
-  // do not fit the registers of two waves a SIMD
-  if (p.row_waves == 1 && p.row_tiles == 1 && blocks * splits <= 256 && c.bits * c.head_dim <= 1024) p.key_waves = 8;
+  // With a block or less for a compute unit, 8 waves a block take half the steps
+  // (8 / 4 waves: one sequence of 32768 keys, 4 rows, 23 / 27 us; 128 pairs, 6143
+  // keys, 40 rows, 8 bits, 56 / 70 us); 256 elements of 8 bits do not fit the
+  // registers of two waves a SIMD.
+  if (p.row_waves == 1 && blocks * splits <= 256 && c.bits * c.head_dim <= 1024) p.key_waves = 8;
   p.split_tiles = (int32_t)per;
   p.splits = (int32_t)((tiles + per - 1) / per);
   return p;

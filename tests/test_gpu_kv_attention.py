@@ -318,6 +318,7 @@ def test_two_graphs_with_their_own_workspaces():
     (270, 4, 1, 128, 4, 128), (270, 8, 1, 64, 8, 32), (270, 3, 1, 256, 8, 64),     # one tile of rows, 4 waves
     (140, 6, 4, 128, 4, 64), (20, 6, 4, 128, 4, 64),                               # 24 rows, many and few pairs
     (140, 5, 8, 256, 4, 128), (140, 7, 8, 256, 8, 32), (20, 10, 10, 256, 4, 64),   # 256 elements, 40, 56 and 100 rows
+    (20, 10, 4, 64, 8, 32), (20, 10, 4, 128, 8, 32),                               # 40 rows, few pairs
     (140, 13, 8, 64, 4, 64), (140, 13, 8, 128, 8, 128), (5, 43, 3, 64, 8, 64),     # 104 and 129 rows
 ])
 def test_forms_chosen_by_pairs_and_rows(seqs, per, new, D, bits, group):
@@ -328,7 +329,7 @@ def test_forms_chosen_by_pairs_and_rows(seqs, per, new, D, bits, group):
     Case(lens, [min(new, n) for n in lens], heads=1, per=per, D=D, bits=bits, group=group, seed=30).run_and_check()
 
 
-@pytest.mark.parametrize("D,new", [(64, 300), (128, 300), (256, 150)])
+@pytest.mark.parametrize("D,new", [(64, 300), (128, 300), (256, 150), (128, 40), (64, 120)])
 def test_many_rows_split_and_joined(D, new):
     c = Case([4200, 170], [new, 60], heads=1, per=1, D=D, group=64, page=64, seed=31)
     assert B.echo_kv_workspace_bytes(c.cache, c.batch(), 1) > 0
