@@ -125,6 +125,16 @@ def test_rows_that_see_nothing_become_zero():
     assert (out[:11] == 0).all() and (out[11:] == 33.0).all()
 
 
+def test_the_widest_window_with_rows_before_the_first_position():
+    """A window of 2^31 - 1 hides nothing, also beside rows whose position is negative."""
+    c = Case([40], [60], seed=28)
+    want = c.run()
+    assert torch.equal(c.run(window=2 ** 31 - 1), want) and (want[:20] == 0).all()
+    assert torch.equal(c.run(window=2 ** 31 - 1, sinks=2 ** 31 - 1), want)
+    c.new, c.q = [40], c.q[20:]
+    c.check(want[20:])
+
+
 def test_a_page_that_is_none_hides_its_keys():
     c = Case([100], [1], page=16, seed=6)
     batch = c.batch()
