@@ -313,6 +313,8 @@ class KVCache:
             if tuple(t.shape) != shape or t.dtype != dtype or t.device != self.device:
                 raise ValueError(f"{name}: expected {dtype} {shape} on {self.device}, "
                                  f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
         return echo_kv_cache(self.bits, self.group, self.head_dim, heads, slots, 0, pages, _ptr(self.k_codes),
                              _ptr(self.v_codes), _ptr(self.k_params), _ptr(self.v_params))
 
@@ -336,8 +338,8 @@ class KVBatch:
                 or self.kv_len.dim() != 1:
             raise ValueError("a batch is row_start [seqs + 1], kv_len [seqs] and page_table [seqs, entries]")
         for t in (self.row_start, self.kv_len, self.page_table):
-            if t.dtype != torch.int32 or t.device != device:
-                raise ValueError(f"a batch's arrays are int32 on the cache's device {device}")
+            if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+                raise ValueError(f"a batch's arrays are contiguous int32 on the cache's device {device}")
         return echo_kv_batch(seqs, self.rows, self.max_new, self.max_len, self.page_table.shape[1],
                              _ptr(self.row_start), _ptr(self.kv_len), _ptr(self.page_table))
 
@@ -436,8 +438,8 @@ def prepare_kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, out: t
         with torch.cuda.stream(_as_stream(device, stream)):
             workspace = torch.zeros(echo_kv_workspace_bytes(cache, batch, q_heads, causal, window, sinks),
                                     dtype=torch.uint8, device=device)
-    elif workspace.dtype != torch.uint8 or workspace.device != device:
-        raise ValueError(f"workspace: uint8 on {device}")
+    elif workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: contiguous uint8 on {device}")
     return _PreparedOn(load_library().echo_kv_attention,
                        (ctypes.byref(c), ctypes.byref(b), q_heads, ctypes.byref(qr), ctypes.byref(outr), scale,
                         int(causal), window, sinks, _ptr(workspace) or None, workspace.numel(), st),
@@ -459,10 +461,6 @@ def echo_kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, out: torc
                       stream=None):
     """q, out: [rows, q_heads, head_dim], both bf16 or both fp16.  Without a
     workspace one is allocated for this call on its stream."""
-    if workspace is None:
-        with torch.cuda.stream(_as_stream(cache.device, stream)):
-            workspace = torch.zeros(echo_kv_workspace_bytes(cache, batch, q.shape[1], causal, window, sinks),
-                                    dtype=torch.uint8, device=cache.device)
     prepare_kv_attention(cache, batch, q, out, scale, causal, window, sinks, workspace, stream)()
 
 

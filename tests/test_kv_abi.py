@@ -224,3 +224,17 @@ def test_binding_refuses_what_the_library_cannot_see():
             bad.desc(torch.device("cpu"))
     with pytest.raises(ValueError, match="k_params"):
         B.KVCache(4, 64, 128, c.k_codes, c.v_codes, c.k_params, c.v_params).desc()
+
+
+def test_binding_refuses_views_whose_strides_it_cannot_pass_on():
+    c = B.alloc_kv_cache(4, 16, 2, 128, device="cpu")
+    wide = B.alloc_kv_cache(4, 32, 2, 128, device="cpu")
+    b = B.KVBatch(torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32),
+                  torch.zeros(2, 4, dtype=torch.int32), rows=6, max_new=4, max_len=64)
+    for bad in (B.KVBatch(b.row_start, b.kv_len, torch.zeros(2, 8, dtype=torch.int32)[:, :4], 6, 4, 64),
+                B.KVBatch(b.row_start, torch.zeros(4, dtype=torch.int32)[::2], b.page_table, 6, 4, 64),
+                B.KVBatch(torch.zeros(6, dtype=torch.int32)[::2], b.kv_len, b.page_table, 6, 4, 64)):
+        with pytest.raises(ValueError, match="contiguous"):
+            bad.desc(torch.device("cpu"))
+    with pytest.raises(ValueError, match="v_codes must be contiguous"):
+        B.KVCache(4, 128, 128, c.k_codes, wide.v_codes[:, :, :16], c.k_params, c.v_params).desc()
