@@ -21,28 +21,25 @@ namespace kv {
 
 constexpr int kThreads = 256;
 
-template <int CTRL>
-__device__ __forceinline__ float dpp(float v) {
-  return __builtin_bit_cast(
-      float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
-}
+// One step of a minimum and a maximum between lanes.  Written out because the
+// compiler keeps the move between lanes apart from the minimum and quiets its
+// result first: 9 instructions a step in place of 3 (a lane exchange reads what
+// the vector unit wrote two cycles before at the latest, hence the s_nop).
+#define ECHO_KV_MINMAX(LANES)                                       \
+  asm volatile("s_nop 1\n"                                          \
+               "v_min_f32_dpp %0, %0, %0 " LANES " row_mask:0xf bank_mask:0xf bound_ctrl:0\n" \
+               "v_max_f32_dpp %1, %1, %1 " LANES " row_mask:0xf bank_mask:0xf bound_ctrl:0"   \
+               : "+v"(mn), "+v"(mx))
 
 // Minimum and maximum over aligned runs of LANES = 4, 8 or 16 lanes.
 template <int LANES>
 __device__ __forceinline__ void run_minmax(float& mn, float& mx) {
-  mn = fminf(mn, dpp<0xB1>(mn));     // quad_perm [1,0,3,2]
-  mx = fmaxf(mx, dpp<0xB1>(mx));
-  mn = fminf(mn, dpp<0x4E>(mn));     // quad_perm [2,3,0,1]
-  mx = fmaxf(mx, dpp<0x4E>(mx));
-  if constexpr (LANES >= 8) {
-    mn = fminf(mn, dpp<0x141>(mn));  // lane i <-> 7-i within 8
-    mx = fmaxf(mx, dpp<0x141>(mx));
-  }
-  if constexpr (LANES >= 16) {
-    mn = fminf(mn, dpp<0x140>(mn));  // lane i <-> 15-i within 16
-    mx = fmaxf(mx, dpp<0x140>(mx));
-  }
+  ECHO_KV_MINMAX("quad_perm:[1,0,3,2]");
+  ECHO_KV_MINMAX("quad_perm:[2,3,0,1]");
+  if constexpr (LANES >= 8) ECHO_KV_MINMAX("row_half_mirror");   // lane i <-> 7-i within 8
+  if constexpr (LANES >= 16) ECHO_KV_MINMAX("row_mirror");       // lane i <-> 15-i within 16
 }
+#undef ECHO_KV_MINMAX
 
 template <int DT>
 __device__ __forceinline__ void load8(const void* p, int64_t e, u32x4 (&w)[DT == kKvF32 ? 2 : 1]) {
@@ -121,7 +118,8 @@ __device__ __forceinline__ void encode8(const float* x, const QParams& q, uint32
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float t = __builtin_amdgcn_fmed3f((x[i] - q.zf) * q.inv, 0.0f, qmax);   // NaN: 0
-    b[i / 4] = __builtin_amdgcn_cvt_pk_u8_f32(rintf(t), i % 4, b[i / 4]);
+    // the conversion rounds half to even
+    b[i / 4] = __builtin_amdgcn_cvt_pk_u8_f32(t, i % 4, b[i / 4]);
   }
   if constexpr (BITS == 8) {
     w[0] = b[0];
