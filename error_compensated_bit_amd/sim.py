@@ -118,6 +118,11 @@ def attention_site(cfg, r: Ranks, a: AttentionRanks, batch: B.KVBatch, qs, ks, v
     the output projection; the partial products are summed by one call.
     qs, ks, vs: the ranks' projected rows [batch.rows, heads, head_dim];
     r: ranks with messages of batch.rows * hidden elements."""
+    if r.n != batch.rows * a.projections[0].shape[1] or not r.P == len(a.caches) == len(qs) == len(ks) == len(vs):
+        raise ValueError(f"{batch.rows} rows of {a.projections[0].shape[1]} from {len(a.caches)} ranks do not make "
+                         f"the messages of {r.n} elements of {r.P} ranks")
+    if batch.rows > a.attended[0].shape[0]:
+        raise ValueError(f"buffers of {a.attended[0].shape[0]} rows, a batch of {batch.rows}")
     for p in range(r.P):
         att, part = a.attended[p][:batch.rows], a.partial[p][:batch.rows]
         B.echo_kv_write(a.caches[p], batch, ks[p], vs[p])

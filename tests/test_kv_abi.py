@@ -10,6 +10,7 @@ import pytest
 import torch
 
 from error_compensated_bit_amd import binding as B
+from error_compensated_bit_amd import sim
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 A = 0x10000
@@ -238,3 +239,17 @@ def test_binding_refuses_views_whose_strides_it_cannot_pass_on():
             bad.desc(torch.device("cpu"))
     with pytest.raises(ValueError, match="v_codes must be contiguous"):
         B.KVCache(4, 128, 128, c.k_codes, wide.v_codes[:, :, :16], c.k_params, c.v_params).desc()
+
+
+def test_attention_site_refuses_a_batch_that_is_not_the_messages():
+    rows, hidden = 6, 32
+    a = sim.AttentionRanks([None, None], [torch.zeros(128, hidden)] * 2, None, [torch.zeros(rows, 1, 128)] * 2,
+                           [torch.zeros(rows, hidden)] * 2)
+    batch = B.KVBatch(None, None, None, rows, rows, rows)
+    x = [torch.zeros(rows, 1, 128)] * 2
+    for r, b, q in ((sim.Ranks(2, rows * hidden + 1, [], [], [], None), batch, x),
+                    (sim.Ranks(2, rows * hidden, [], [], [], None), batch, x[:1]),
+                    (sim.Ranks(3, rows * hidden, [], [], [], None), batch, x),
+                    (sim.Ranks(2, 7 * hidden, [], [], [], None), B.KVBatch(None, None, None, 7, 7, 7), x)):
+        with pytest.raises(ValueError):
+            sim.attention_site(None, r, a, b, q, x, x, 0.1)
