@@ -725,7 +725,7 @@ __device__ __forceinline__ float get_shared(const float* p) {
 // Behind the stores of a split's results: the last of the splits of a block's
 // rows to arrive joins them all, in the order of the splits.  It leaves the
 // counter 0 for the next call.  `word`: LDS.
-template <int D, int THREADS>
+template <int D, int THREADS, int kBatch>
 __device__ __forceinline__ void join_splits(const KvAttnArgs& a, const Block& k, int block_rows, uint32_t* word) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's results have arrived
   __syncthreads();                                    // and the other waves'
@@ -744,14 +744,31 @@ __device__ __forceinline__ void join_splits(const KvAttnArgs& a, const Block& k,
     const float* ml = a.part_ml + at * 2;
     const float* po = a.part_o + at * D + run * 8;
     float top = kLowest, sum = 0.0f, v[8] = {};
-#pragma unroll 4
-    for (int s = 0; s < k.active; ++s) top = fmaxf(top, get_shared(ml + 2 * s));
-#pragma unroll 4
-    for (int s = 0; s < k.active; ++s) {
-      const float f = __builtin_amdgcn_exp2f(get_shared(ml + 2 * s) - top);
-      sum = fmaf(get_shared(ml + 2 * s + 1), f, sum);
+    // kBatch splits' loads in flight together; behind the last split that one again, with weight 0
+    for (int s0 = 0; s0 < k.active; s0 += kBatch) {
+      float m[kBatch], l[kBatch], o[kBatch][8], t = top;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = fmaf(get_shared(po + (int64_t)s * D + e), f, v[e]);
+      for (int i = 0; i < kBatch; ++i) {
+        const int s = min(s0 + i, k.active - 1);
+        m[i] = get_shared(ml + 2 * s);
+        l[i] = get_shared(ml + 2 * s + 1);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[i][e] = get_shared(po + (int64_t)s * D + e);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) t = fmaxf(t, m[i]);
+      const float down = __builtin_amdgcn_exp2f(top - t);
+      top = t;
+      sum *= down;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= down;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float f = s0 + i < k.active ? __builtin_amdgcn_exp2f(m[i] - top) : 0.0f;
+        sum = fmaf(l[i], f, sum);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = fmaf(o[i][e], f, v[e]);
+      }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const int i = row / a.heads_per_kv, h = k.hk * a.heads_per_kv + row - i * a.heads_per_kv;
@@ -888,7 +905,7 @@ __global__ __launch_bounds__(NW * 64, few_min_waves(BITS, D, G, NT)) void k_kv_a
       for (int e = 0; e < 8; ++e) put_shared(a.part_o + at * D + run * 8 + e, v[e]);
     }
   }
-  if (k.active > 1) join_splits<D, NW * 64>(a, k, Lds::kRows, reinterpret_cast<uint32_t*>(lds.top));
+  if (k.active > 1) join_splits<D, NW * 64, 4>(a, k, Lds::kRows, reinterpret_cast<uint32_t*>(lds.top));
 }
 
 // ------------------------------------------------------------------ many rows
@@ -1091,7 +1108,7 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void k_kv_attention_many(
         for (int j = 0; j < 4; ++j) put_shared(a.part_o + at * D + d * 16 + quad * 4 + j, w.o[i][d][j]);
     }
   }
-  if (k.active > 1) join_splits<D, NW * 64>(a, k, Lds::kRows, reinterpret_cast<uint32_t*>(lds.top));
+  if (k.active > 1) join_splits<D, NW * 64, 1>(a, k, Lds::kRows, reinterpret_cast<uint32_t*>(lds.top));
 }
 
 }  // namespace kv
