@@ -54,6 +54,14 @@ KvPlan kv_attention_plan(const KvCache& c, const KvBatch& b, int heads_per_kv, i
   // 512, 125 with 1536; one of 512 keys: 8.3 us whole, 9.7 in two).
   int64_t splits = 256 / blocks;
   if (splits > tiles / 16) splits = tiles / 16;
+  // One block joins the parts of its rows: about 2 us for every split and 4096
+  // elements where each wave has its own rows, a quarter of that where they share
+  // them, against 1.2 and 0.15 us for a tile of keys.  The sum is least where
+  // splits^2 * passes = tiles * 0.6 (0.3); us without / with this bound: 256 rows
+  // after 16384 keys 493 / 218, 400 rows after 131072 keys 1852 / 533, 100 rows
+  // after 32768 keys 130 / 57, one row after 131072 keys 62 / 28.
+  const int64_t passes = (block_rows * c.head_dim / 8 + 511) / 512;
+  while (splits > 1 && splits * splits * passes * 10 > tiles * (p.row_waves == 1 ? 3 : 6)) --splits;
   if (splits < 1 || blocks > kKvCounters) splits = 1;
   const int64_t per = (tiles + splits - 1) / splits;
   // With a block or less for a compute unit, 8 waves a block take half the steps

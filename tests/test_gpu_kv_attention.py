@@ -350,7 +350,7 @@ def test_one_workspace_for_calls_that_follow_each_other():
     """A workspace of the largest call serves smaller ones in between; a call
     leaves its counters at 0; one that is too small is refused."""
     cases = [Case([4000, 700], [3, 1], heads=1, per=4, seed=32), Case([2500], [1], heads=2, per=2, D=64, group=64, seed=33),
-             Case([1500, 3, 1200], [40, 3, 40], heads=1, per=8, seed=34)]
+             Case([6000, 3, 1200], [40, 3, 40], heads=1, per=8, seed=34)]
     sizes = [B.echo_kv_workspace_bytes(c.cache, c.batch(), c.heads * c.per) for c in cases]
     assert min(sizes) > 0 and len(set(sizes)) == 3
     want = [c.run() for c in cases]
