@@ -211,7 +211,7 @@ int echo_kv_attention(const echo_kv_cache* cache, const echo_kv_batch* batch, in
   // score of minus infinity stays one
   a.scale_log2 = scale == 0.0f ? 0x1p-100f : (float)((double)scale * 1.4426950408889634);
   a.causal = causal;
-  a.window = window < kMaxRows ? window : kMaxRows;   // no two positions are further apart
+  a.window = window;
   a.sinks = sinks;
   a.counters = static_cast<uint32_t*>(workspace);
   a.part_o = static_cast<float*>(workspace) + kKvCounters;

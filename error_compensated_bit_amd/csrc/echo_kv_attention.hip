@@ -431,9 +431,9 @@ struct Wave {
     for (int t = 0; t < NT; ++t) {
       const int r = first + t * 16 + n, row = row0 + r;
       const bool exists = row < rows;
-      const int pos = sq.len - sq.n + row / a.heads_per_kv;
+      const int pos = (int)((uint32_t)sq.pos + (uint32_t)(row / a.heads_per_kv));   // may wrap where the row does not exist
       hi[t] = !a.causal || !exists ? sq.len - 1 : pos < sq.len ? pos : sq.len - 1;
-      lo[t] = a.window > 0 && exists ? (int)max((int64_t)pos - a.window + 1, (int64_t)0) : 0;
+      lo[t] = exists ? window_start(a.window, pos) : 0;
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) qs[t][g] = from.qs[r][g] * rf;
 #pragma unroll
@@ -679,7 +679,7 @@ __device__ __forceinline__ bool block_of(const KvAttnArgs& a, int block_rows, Bl
   k.row0 = k.rb * block_rows;
   if (k.row0 >= k.rows) return false;
   const int last = min(k.row0 + block_rows, k.rows) - 1;
-  k.span = key_span(a, k.sq.len, k.sq.n, k.row0 / a.heads_per_kv, last / a.heads_per_kv);
+  k.span = key_span(a, k.sq.len, (int64_t)k.sq.len - k.sq.pos, k.row0 / a.heads_per_kv, last / a.heads_per_kv);
   k.active = (k.span.tiles + a.plan.split_tiles - 1) / a.plan.split_tiles;
   k.t0 = k.split * a.plan.split_tiles;
   k.t1 = min(k.t0 + a.plan.split_tiles, k.span.tiles);
@@ -687,9 +687,9 @@ __device__ __forceinline__ bool block_of(const KvAttnArgs& a, int block_rows, Bl
   return k.split == 0 || k.split < k.active;
 }
 __device__ __forceinline__ Bounds bounds_of(const KvAttnArgs& a, const Block& k, int first, int last) {
-  const int p0 = k.sq.len - k.sq.n + first / a.heads_per_kv, p1 = k.sq.len - k.sq.n + last / a.heads_per_kv;
-  return Bounds{a.causal ? p0 : k.sq.len - 1, a.causal ? p1 : k.sq.len - 1,
-                a.window > 0 ? p0 - a.window + 1 : 0, a.window > 0 ? p1 - a.window + 1 : 0};
+  const int p0 = k.sq.pos + first / a.heads_per_kv, p1 = k.sq.pos + last / a.heads_per_kv;
+  return Bounds{a.causal ? p0 : k.sq.len - 1, a.causal ? p1 : k.sq.len - 1, window_start(a.window, p0),
+                window_start(a.window, p1)};
 }
 __device__ __forceinline__ bool tile_seen(const Bounds& r, int tb, int sinks) {
   return tb <= r.hi_max && (tb + kTile > r.lo_min || tb < sinks);

@@ -96,18 +96,23 @@ struct Span {
   __host__ __device__ __forceinline__ int token(int t) const { return t < t1 ? t * kTile : start + (t - t1) * kTile; }
 };
 
-// What the rows of tokens i0 .. i1 (of n new ones) see of a sequence of `len` keys.
-__host__ __device__ __forceinline__ Span key_span(const KvAttnArgs& a, int len, int n, int i0, int i1) {
+// The first key that the window leaves to a row at position p; 32 bits hold it
+// for any p and window.
+__host__ __device__ __forceinline__ int window_start(int window, int p) {
+  return window > 0 && p >= window ? p - window + 1 : 0;
+}
+
+// What the rows of tokens i0 .. i1 see of a sequence of `len` keys whose token 0
+// sits at position len - n.
+__host__ __device__ __forceinline__ Span key_span(const KvAttnArgs& a, int len, int64_t n, int i0, int i1) {
   Span s{0, 0, 0};
+  const int pos = (int)(len - n);
   int end = len;
-  if (a.causal) {
-    end = len - n + i1 + 1;
-    end = end < len ? end : len;
-  }
+  if (a.causal && pos + i1 < len) end = pos + i1 + 1;
   if (end <= 0) return s;
   if (a.window > 0) {
-    const int64_t lo = (int64_t)len - n + i0 - a.window + 1;
-    const int first = lo > 0 ? (int)lo / kTile * kTile : 0;
+    int first = window_start(a.window, pos + i0);
+    first = (first < len ? first : len) / kTile * kTile;   // rows behind the keys may see only the first ones
     const int sinks = a.sinks < end ? a.sinks : end;
     const int s_end = (sinks + kTile - 1) / kTile * kTile;
     if (s_end < first) {
@@ -115,28 +120,35 @@ __host__ __device__ __forceinline__ Span key_span(const KvAttnArgs& a, int len, 
       s.start = first;
     }
   }
-  s.tiles = s.t1 + (end - s.start + kTile - 1) / kTile;
+  s.tiles = s.t1 + (end > s.start ? (end - s.start + kTile - 1) / kTile : 0);
   return s;
 }
 
-// One sequence's rows: the first one's index in the packed arrays, how many it
-// has, how many of them the call computes, and its keys.  Any contents of the
-// device arrays give ranges inside the caller's bounds.
+// One sequence's rows: the first one's index in the packed arrays and position,
+// how many of them the call computes, and its keys.  The rows are the last
+// positions of kv_len, as in row_place(), also where max_len or the page table
+// leaves fewer keys.  Any contents of the device arrays give ranges inside the
+// caller's bounds, and positions inside 32 bits: -2^31 < kv_len - row_end + row
+// < 2^31 for rows below row_end.
 struct Seq {
-  int first, n, computed, len;
+  int first, n, computed, len, pos;
 };
 __host__ __device__ __forceinline__ Seq sequence(const KvAttnArgs& a, int b) {
   Seq s;
-  int lo = a.b.row_start[b], hi = a.b.row_start[b + 1];
+  int lo = a.b.row_start[b];
+  const int end = a.b.row_start[b + 1];
+  int hi = end;
   lo = lo < 0 ? 0 : lo > a.b.rows ? a.b.rows : lo;
   hi = hi < lo ? lo : hi > a.b.rows ? a.b.rows : hi;
   s.first = lo;
   s.n = hi - lo;
   s.computed = s.n < a.b.max_new ? s.n : a.b.max_new;
-  const int64_t room = a.b.table_stride << a.c.page_shift;
-  int64_t len = a.b.kv_len[b];
-  len = len < 0 ? 0 : len > a.b.max_len ? a.b.max_len : len;
-  s.len = (int)(len < room ? len : room);
+  // in 32 bits: a 64-bit comparison would take its operands out of the scalar registers
+  const int len = a.b.kv_len[b] < 0 ? 0 : a.b.kv_len[b];   // below 0 every position is, as with 0
+  s.pos = s.n > 0 ? len - (end - lo) : 0;
+  const int entries = (int)a.b.table_stride;   // at most 2^30
+  const int room = entries > a.b.max_len >> a.c.page_shift ? a.b.max_len : entries << a.c.page_shift;
+  s.len = len < room ? len : room;
   return s;
 }
 

@@ -212,8 +212,9 @@ size_t echo_state_bytes(int64_t n, int state_dtype);
  * The three device arrays cannot be checked by the host.  Whatever they hold,
  * no call leaves the caller's buffers: a row outside every sequence, a position
  * below 0, from max_len on or past the page table, and an entry that names no
- * page are passed over (not written, not read, not attended to).  Rows behind
- * the last sequence keep their contents.  Two rows of one call in the same slot
+ * page are passed over (not written, not read, not attended to); a query row
+ * keeps its position there and sees the keys that are left.  Rows behind the
+ * last sequence keep their contents.  Two rows of one call in the same slot
  * (a page in two places of the table) leave that slot undefined.
  */
 typedef struct echo_kv_cache {
@@ -234,7 +235,7 @@ typedef struct echo_kv_batch {
     int32_t seqs;                /* sequences, at most 65535 */
     int32_t rows;                /* rows of the packed arrays, at most 2^30 */
     int32_t max_new;             /* no sequence has more rows (attention: later ones are not computed) */
-    int32_t max_len;             /* no kv_len is larger (a larger one is cut to it) */
+    int32_t max_len;             /* no kv_len is larger (of a longer sequence, positions from max_len on are passed over) */
     int64_t table_stride;        /* page-table entries per sequence */
     const int32_t* row_start;    /* device, seqs + 1, ascending */
     const int32_t* kv_len;       /* device, seqs: positions in use, this call's rows included */
