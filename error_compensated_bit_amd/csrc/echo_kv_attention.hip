@@ -342,12 +342,15 @@ struct ParamWords {
       word[i] = from[(run & 1 ? row1 : row0) * kGroups + w % (16 * kGroups)];
     }
   }
-  // Words of tokens that are not there become 0: their slots may hold anything.
-  __device__ __forceinline__ void clear_missing(int tb, int len, uint32_t ok) {
+  // Words of keys that no row of the block sees become 0: nobody need have
+  // written their slots, and what lies there would reach the products (0 * NaN)
+  // and the normaliser of the steps.  The rows see the keys from `lo` to `end`
+  // and the first `sinks`.
+  __device__ __forceinline__ void clear_unseen(int tb, int end, int lo, int sinks, uint32_t ok) {
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
       const int w = i * 64 + threadIdx.x % 64, s = w / (16 * kGroups) & 1, j = tb + 16 * s + w % (16 * kGroups) / kGroups;
-      if (!(j < len && (ok >> s & 1u))) word[i] = 0u;
+      if (!(j < end && (j >= lo || j < sinks) && (ok >> s & 1u))) word[i] = 0u;
     }
   }
   __device__ __forceinline__ float largest_step() const {   // of this lane's values
@@ -841,7 +844,7 @@ __global__ __launch_bounds__(NW * 64, few_min_waves(BITS, D, G, NT)) void k_kv_a
     if (tile_seen(r, tb[0], a.sinks)) {
       const uint32_t ok[1] = {page_ok};
       const bool whole = tile_whole(r, tb[0], k.sq.len, page_ok, a.sinks);
-      if (!whole) words.clear_missing(tb[0], k.sq.len, page_ok);
+      if (!whole) words.clear_unseen(tb[0], k.span.end, r.lo_min, a.sinks, page_ok);
       if (scale.see(words.largest_step())) w.set_scale(scale.einv);
       wave_sync();
       words.put(params, rf, scale.einv);
@@ -1038,12 +1041,22 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void k_kv_attention_many(
 #pragma unroll
     for (int i = 0; i < kMine; ++i) codes[i].unpack(to.tile[mine(i)], quarter);
     if (wave == 0) {
-      float top = 0.0f;
+      // the first wave has the block's first row, whose window reaches back the furthest
+      // (2048 rows after 16384 keys: one branch for the step's tiles 664 us, one
+      // a tile 667, clearing without a branch 669)
+      bool seen = true;   // all keys, as in most steps of a long sequence
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
-        words[u].clear_missing(token(t + u), k.sq.len, ok[u]);
-        top = fmaxf(top, words[u].largest_step());
+        const int tb = token(t + u);
+        seen &= tb + kTile <= k.span.end && tb >= r.lo_min && ok[u] == 3u;
       }
+      if (!seen) {
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) words[u].clear_unseen(token(t + u), k.span.end, r.lo_min, a.sinks, ok[u]);
+      }
+      float top = 0.0f;
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) top = fmaxf(top, words[u].largest_step());
       scale.see(top);
 #pragma unroll
       for (int u = 0; u < SUB; ++u) words[u].put(to.tile[u].params, rf, scale.einv);

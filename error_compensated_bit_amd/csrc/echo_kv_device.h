@@ -90,9 +90,9 @@ constexpr float kLowest = -3.0e38f;  // running maximum before any key: below ev
 
 // The keys a block's rows can see, as tiles: those below `t1` start at 0, the
 // others at `start`; a window skips what lies between the first keys (sinks)
-// and the earliest row's window.
+// and the earliest row's window.  The rows see no key from `end` on.
 struct Span {
-  int t1, start, tiles;
+  int t1, start, tiles, end;
   __host__ __device__ __forceinline__ int token(int t) const { return t < t1 ? t * kTile : start + (t - t1) * kTile; }
 };
 
@@ -105,11 +105,12 @@ __host__ __device__ __forceinline__ int window_start(int window, int p) {
 // What the rows of tokens i0 .. i1 see of a sequence of `len` keys whose token 0
 // sits at position len - n.
 __host__ __device__ __forceinline__ Span key_span(const KvAttnArgs& a, int len, int64_t n, int i0, int i1) {
-  Span s{0, 0, 0};
+  Span s{0, 0, 0, 0};
   const int pos = (int)(len - n);
   int end = len;
   if (a.causal && pos + i1 < len) end = pos + i1 + 1;
   if (end <= 0) return s;
+  s.end = end;
   if (a.window > 0) {
     int first = window_start(a.window, pos + i0);
     first = (first < len ? first : len) / kTile * kTile;   // rows behind the keys may see only the first ones
