@@ -265,7 +265,9 @@ struct QueryRows {
       o = f16x8{e[0], e[2], e[1], e[3], e[4], e[6], e[5], e[7]};
     }
     op[r / 16][run / 4][run % 4 * 16 + r % 16] = o;
-    if (run % (G / 8) == 0) qs[r][run / (G / 8)] = sum * 0x1p-24f;
+    // an infinite or NaN element makes every score of its row NaN here (infinity
+    // less infinity in the softmax), also where all would be minus infinity
+    if (run % (G / 8) == 0) qs[r][run / (G / 8)] = sum * 0x1p-24f + (sum - sum);
   }
 
   // All rows with one power of two, from the largest finite element of the

@@ -1,0 +1,86 @@
+"""Queries of one call whose sizes differ by many powers of two, scales at the
+ends of binary32, and queries that are no numbers: no row's query changes
+another row's result.
+
+Bound: kv_attend64.attend_at's.  An element of a query enters the products with
+an error of 2^-25 of its row's largest element at most, a score with 2^-25 max|q|
+sum_d |c_d s|.  For drawn rows (max|q| about 4.5, c s about 5 at most, mean |k|
+|q| about 1) that is 23 D 2^-25, a twelfth of the D (D + 8) 2^-23 that the bound's
+first term allows at 64 elements, less above."""
+import numpy as np
+import pytest
+import torch
+
+import kv_testutil as U
+from error_compensated_bit_amd import binding as B
+from kv_attend64 import Sequences
+
+pytestmark = pytest.mark.gpu
+FORMS = [(128, 4, 128), (64, 4, 32), (256, 4, 128), (128, 8, 64), (64, 8, 64), (256, 8, 32)]
+
+
+def run(s, q, n, scale=None, **mask):
+    q = q.to(s.device)
+    out = torch.full_like(q, 33.0)
+    B.echo_kv_attention(s.cache, s.batch([n], s.lens), q, out, s.scale if scale is None else scale, **mask)
+    torch.cuda.synchronize()
+    return out
+
+
+def filled(n, D=128, bits=4, group=128, dtype="bf16", seed=0, length=150, **kw):
+    s = Sequences([length], D=D, bits=bits, group=group, dtype=dtype, seed=seed, **kw)
+    s.write([(0, length)])
+    return s, s.queries(n)
+
+
+def check(s, out, q, n, rows=None, **kw):
+    rows = np.arange(n) if rows is None else np.asarray(rows)
+    s.check(out[rows], q[rows], 0, s.lens[0] - n + rows, s.lens[0], **kw)
+
+
+@pytest.mark.parametrize("n", [3, 40])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("D,bits,group", [(128, 4, 128), (64, 8, 32), (256, 4, 64)])
+def test_rows_that_are_no_numbers(D, bits, group, bad, n):
+    """A NaN or infinite element makes its own row NaN and no other.  The others
+    are right within the bound, not bit for bit: a row whose maximum is not
+    settled lets its whole wave's maxima rise, and a probability rounds to f16
+    relative to its row's."""
+    s, q = filled(n, D, bits, group, seed=6)
+    s.kv[0][0] = s.kv[0][0].abs() + 1.0                 # keys whose products with an infinity have one sign
+    s.write([(0, 150)])
+    q[1, 3, 7] = bad
+    out = run(s, q, n)
+    assert out[1, 3].isnan().all()
+    q[1, 3] = 0
+    clean = run(s, q, n)
+    check(s, clean, q, n)
+    out[1, 3] = clean[1, 3]
+    check(s, out, q, n)
+
+
+@pytest.mark.parametrize("n", [3, 40])
+@pytest.mark.parametrize("D,bits,group", [(128, 4, 128), (64, 8, 32), (256, 4, 64)])
+def test_a_row_whose_scores_are_all_minus_infinity(D, bits, group, n):
+    """Infinity less infinity in the softmax: NaN, not the 0 of a row that sees nothing."""
+    s, q = filled(n, D, bits, group, seed=6)
+    s.kv[0][0] = s.kv[0][0].abs() + 1.0
+    s.kv[0][0][:, :, 7] += 2.0                          # no key's code is 0 there
+    s.write([(0, 150)])
+    codes, _, _ = U.quantize(U.host64(s.kv[0][0]), bits, group)
+    assert (codes[:, :, 7] > 0).all()
+    q[1, 3, 7] = -float("inf")
+    out = run(s, q, n)
+    assert out[1, 3].isnan().all()
+    q[1, 3] = 0
+    out[1, 3] = run(s, q, n)[1, 3]
+    check(s, out, q, n)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_rows_that_are_no_numbers_and_see_nothing(bad):
+    s, q = filled(3, seed=7)
+    q[:] = bad
+    out = torch.full_like(q, 33.0).to(s.device)
+    B.echo_kv_attention(s.cache, s.batch([3], [0], max_len=64), q.to(s.device), out, s.scale)
+    assert (out == 0).all()
