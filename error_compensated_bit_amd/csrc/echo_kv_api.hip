@@ -207,9 +207,7 @@ int echo_kv_attention(const echo_kv_cache* cache, const echo_kv_batch* batch, in
   a.q = rows_of(q);
   a.out = rows_of(out);
   a.heads_per_kv = q_heads / cache->kv_heads;
-  // 0 is taken as 2^-100: every visible key weighs the same, and a masked
-  // score of minus infinity stays one
-  a.scale_log2 = scale == 0.0f ? 0x1p-100f : (float)((double)scale * 1.4426950408889634);
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
   a.causal = causal;
   a.window = window;
   a.sinks = sinks;

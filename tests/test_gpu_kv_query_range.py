@@ -39,6 +39,14 @@ def check(s, out, q, n, rows=None, **kw):
 
 
 @pytest.mark.parametrize("n", [3, 40])
+def test_scale_zero_weighs_every_key_the_same(n):
+    """... also for queries of 2^100 and more."""
+    s, q = filled(n, seed=5)
+    q = (q.float() * 2.0 ** 100).to(torch.bfloat16)
+    check(s, run(s, q, n, scale=0.0), q, n, scale=0.0)
+
+
+@pytest.mark.parametrize("n", [3, 40])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("D,bits,group", [(128, 4, 128), (64, 8, 32), (256, 4, 64)])
 def test_rows_that_are_no_numbers(D, bits, group, bad, n):
