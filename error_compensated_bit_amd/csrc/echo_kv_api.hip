@@ -207,7 +207,7 @@ int echo_kv_attention(const echo_kv_cache* cache, const echo_kv_batch* batch, in
   a.q = rows_of(q);
   a.out = rows_of(out);
   a.heads_per_kv = q_heads / cache->kv_heads;
-  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.scale_log2 = (float)frexp((double)scale * 1.4426950408889634, &a.scale_exp);   // the product may pass FLT_MAX
   a.causal = causal;
   a.window = window;
   a.sinks = sinks;

@@ -298,8 +298,7 @@ struct QueryRows {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < THREADS / 64; ++i) top = fmaxf(top, tops[i]);
-    const int field = __builtin_amdgcn_readfirstlane((int)(__float_as_uint(top) >> 23));
-    const int up = field == 0 ? 0 : 14 - (field - 127);
+    const int up = __builtin_amdgcn_readfirstlane(15 - __builtin_amdgcn_frexp_expf(top));
 #pragma unroll
     for (int pass = 0; pass < kPasses; ++pass) {
       const int unit = pass * THREADS + threadIdx.x;
@@ -308,7 +307,7 @@ struct QueryRows {
       widen(raw[pass], a.q.dtype, x);
       put(x, up, unit / kRuns, unit % kRuns);
     }
-    return ldexpf(a.scale_log2, 24 - up);
+    return ldexpf(a.scale_log2, a.scale_exp + 24 - up);
   }
 };
 

@@ -60,7 +60,8 @@ struct KvAttnArgs {
   KvBatch b;
   KvRows q, out;
   int32_t heads_per_kv;   // query heads that share a K/V head
-  float scale_log2;       // softmax scale * log2(e)
+  float scale_log2;       // softmax scale * log2(e) * 2^-scale_exp: 0, or 1/2 to 1 in size
+  int32_t scale_exp;
   int32_t causal, window, sinks;
   KvPlan plan;
   uint32_t* counters;        // arrived splits of every (sequence, K/V head, block of rows); 0 between calls

@@ -12,7 +12,13 @@ from error_compensated_bit_amd import binding as B
 def attend_at(q, pos, k, v, causal, window, sinks, scale, spread, there=None):
     """Rows q [n, Hq, D] at positions pos [n] over the keys and values
     [length, Hk, D]; there [length]: which keys exist.  Returns the outputs and
-    kv_testutil.attend's bound (see there for its derivation)."""
+    kv_testutil.attend's bound (see there for its derivation) with one term more.
+    A probability of 1 enters the products as 2^10 at least, a step s as s / E with
+    the power of two E above the largest step S, E <= 2 S.  Subnormal halves are
+    off by 2^-25 at most, so each key adds 2^-35 |zero + h step| <= 2^-35 (max|v| + S h)
+    and 2^-35 2 S |code - h| <= 2^-35 2 S h at most, h = 2^(bits - 1), S h = max(spread)
+    (some code of the group with the largest step is 0).  Where one key has all the
+    weight and its value is 0, nothing else is left."""
     n, Hq, D = q.shape
     length, Hk = k.shape[:2]
     out, bound = np.zeros(q.shape), np.zeros(q.shape)
@@ -30,7 +36,8 @@ def attend_at(q, pos, k, v, causal, window, sinks, scale, spread, there=None):
             w /= w.sum()
             out[i, h] = w @ vv
             err = size * (D + 8) * 2.0 ** -23 + (len(s) / 32 + 16) * 2.0 ** -23
-            bound[i, h] = 2.0 ** -11 * (w @ sp) + (w * (err + err.max())) @ (np.abs(vv) + 2 * sp)
+            bound[i, h] = 2.0 ** -11 * (w @ sp) + (w * (err + err.max())) @ (np.abs(vv) + 2 * sp) + \
+                len(s) * 2.0 ** -35 * (np.abs(v).max() + 3 * spread.max())
     return out, bound
 
 

@@ -39,6 +39,16 @@ def check(s, out, q, n, rows=None, **kw):
 
 
 @pytest.mark.parametrize("n", [3, 40])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_the_largest_scales(n, sign):
+    """Scales up to the largest binary32 number, beyond which log2(e) would take them."""
+    s, q = filled(n, seed=4)
+    for scale in (1e38, 3e38, 3.4028234e38):
+        small = (q.float() / 3e38 * 8).to(torch.bfloat16)
+        check(s, run(s, small, n, scale=sign * scale), small, n, scale=sign * scale)
+
+
+@pytest.mark.parametrize("n", [3, 40])
 def test_scale_zero_weighs_every_key_the_same(n):
     """... also for queries of 2^100 and more."""
     s, q = filled(n, seed=5)
