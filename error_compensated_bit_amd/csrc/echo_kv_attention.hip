@@ -564,7 +564,9 @@ struct Wave {
         m = fmaxf(m, __shfl_xor(m, 32));
         const bool any = m > -INFINITY;
         // a row's first keys set its maximum, later ones only raise it
-        const float up = !any ? 0.0f : none[i] ? m - kPeak : fmaxf(m - kPeak, 0.0f);
+        float up = !any ? 0.0f : none[i] ? m - kPeak : fmaxf(m - kPeak, 0.0f);
+        // where floats of m's size lie 16 apart, m - kPeak is m - 16, and 2^16 no half
+        up = m - up > kPeak + kSlack ? m : up;
         const float alpha = none[i] ? 1.0f : __builtin_amdgcn_exp2f(-up);   // nothing to scale yet
         mb[i] += up;
         none[i] = none[i] && !any;

@@ -39,6 +39,16 @@ def check(s, out, q, n, rows=None, **kw):
 
 
 @pytest.mark.parametrize("n", [3, 40])
+@pytest.mark.parametrize("far", range(16, 44))
+def test_scores_of_every_size(n, far):
+    """Scores whose binary32 neighbours lie further apart than a probability may
+    exceed the running maximum: results stay finite."""
+    s, q = filled(n, seed=far)
+    q *= 2.0 ** far
+    check(s, run(s, q, n), q, n)
+
+
+@pytest.mark.parametrize("n", [3, 40])
 @pytest.mark.parametrize("sign", [1.0, -1.0])
 def test_the_largest_scales(n, sign):
     """Scales up to the largest binary32 number, beyond which log2(e) would take them."""
