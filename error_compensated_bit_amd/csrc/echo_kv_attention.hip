@@ -224,6 +224,16 @@ __device__ __forceinline__ float run_reduce(float v, Op op) {
   return v;
 }
 
+// op over a wave, the same in all lanes.
+template <typename Op>
+__device__ __forceinline__ float wave_reduce(float v, Op op) {
+  v = run_reduce<32>(v, op);
+  auto lane = [v](int i) {
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), i));
+  };
+  return op(lane(0), lane(32));
+}
+
 // Query rows of a block in LDS, as matrix operands.
 template <int BITS, int D, int G, int ROWS>
 struct QueryRows {
@@ -270,13 +280,24 @@ struct QueryRows {
     if (run % (G / 8) == 0) qs[r][run / (G / 8)] = sum * 0x1p-24f + (sum - sum);
   }
 
-  // All rows with one power of two, from the largest finite element of the
-  // block (a row 2^14 times smaller than another still keeps bf16's bits);
-  // returns the factor from raw scores to log2 units.  top: a float per wave.
+  // All rows, each times a power of two; a row's size is its largest finite
+  // element.  Where no row is 2^10 times smaller than the largest, whose size comes
+  // into [2^14, 2^15), all have that one's power and one factor from raw scores to
+  // log2 units, which is returned.  Else (`uneven`) every row has its own power,
+  // which brings its own size there, and that factor times factor[row].  Either
+  // way an element is off by 2^-25 of its row's size at most (4-bit codes: an odd
+  // one enters as a sixteenth, and halves end at 2^-24).
+  // A row's whole factor is kept to 2^100, so that products with a step are finite:
+  // beyond (size times scale past 2^91) two scores are equal or differ by 2^30 and
+  // more, cut or not (elements go down to 2^-25 of the size, keys to 2^-24), and one
+  // key has all the weight.  Below 2^-80 it is kept too: scores under 2^-50 weigh
+  // the same.
+  // tops: two floats per wave.
   template <int THREADS>
-  __device__ __forceinline__ float stage_together(const KvAttnArgs& a, const Seq& sq, int hk, int row0, int rows,
-                                                  float* tops) {
-    constexpr int kUnits = ROWS * kRuns, kPasses = (kUnits + THREADS - 1) / THREADS;
+  __device__ __forceinline__ float stage(const KvAttnArgs& a, const Seq& sq, int hk, int row0, int rows, float* tops,
+                                         float (&factor)[ROWS], bool& uneven) {
+    constexpr int kUnits = ROWS * kRuns, kPasses = (kUnits + THREADS - 1) / THREADS, kWaves = THREADS / 64;
+    constexpr int kMost = 100, kLeast = -80, kMiddle = (kMost + kLeast) / 2;
     static_assert(kUnits % 64 == 0, "whole waves");
     u32x4 raw[kPasses];
 #pragma unroll
@@ -284,21 +305,51 @@ struct QueryRows {
       const int unit = pass * THREADS + threadIdx.x;
       raw[pass] = unit < kUnits ? load(a, sq, hk, row0 + unit / kRuns, rows, unit % kRuns) : u32x4{0, 0, 0, 0};
     }
-    float top = 0.0f;
-#pragma unroll
-    for (int pass = 0; pass < kPasses; ++pass) {
-      float x[8];
+    auto larger = [](float u, float v) { return fmaxf(u, v); };
+    auto smaller = [](float u, float v) { return fminf(u, v); };
+    auto largest = [&](int pass) {   // finite element of this lane's 8
+      float x[8], m = 0.0f;
       widen(raw[pass], a.q.dtype, x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = fabsf(x[j]) < INFINITY ? fmaxf(top, fabsf(x[j])) : top;
-    }
+      for (int j = 0; j < 8; ++j) m = fabsf(x[j]) < INFINITY ? fmaxf(m, fabsf(x[j])) : m;
+      return m;
+    };
+    float top = 0.0f, least = INFINITY;   // of all runs of 8 elements; least: of those that are not all 0
 #pragma unroll
-    for (int i = 1; i < 64; i *= 2) top = fmaxf(top, __shfl_xor(top, i));
-    tops[threadIdx.x / 64] = top;
+    for (int pass = 0; pass < kPasses; ++pass) {
+      const float m = largest(pass);
+      top = fmaxf(top, m);
+      least = m > 0.0f ? fminf(least, m) : least;
+    }
+    tops[threadIdx.x / 64] = wave_reduce(top, larger);
+    tops[kWaves + threadIdx.x / 64] = wave_reduce(least, smaller);
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < THREADS / 64; ++i) top = fmaxf(top, tops[i]);
-    const int up = __builtin_amdgcn_readfirstlane(15 - __builtin_amdgcn_frexp_expf(top));
+    for (int i = 0; i < kWaves; ++i) {
+      top = fmaxf(top, tops[i]);
+      least = fminf(least, tops[kWaves + i]);
+    }
+    auto uniform = [](float v) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v))); };
+    top = uniform(top);
+    // a row is as large as its largest run: this is more than it takes, and yet never so for queries of one spread
+    uneven = uniform(least) < top * 0x1p-10f;
+    const int up = 15 - __builtin_amdgcn_frexp_expf(top);
+    if (uneven) {
+#pragma unroll
+      for (int pass = 0; pass < kPasses; ++pass) {
+        const int unit = pass * THREADS + threadIdx.x;
+        const float size = run_reduce<kRuns>(largest(pass), larger);
+        if (unit >= kUnits) break;
+        const int exponent = a.scale_exp + 24 - (size > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(size) : up);
+        const int kept = min(max(exponent, kLeast), kMost);
+        float x[8];
+        widen(raw[pass], a.q.dtype, x);
+        // a row under kLeast comes in smaller; one past kMost stays in f16's range
+        put(x, a.scale_exp + 24 - max(exponent, kLeast), unit / kRuns, unit % kRuns);
+        if (unit % kRuns == 0) factor[unit / kRuns] = ldexpf(1.0f, kept - kMiddle);
+      }
+      return ldexpf(a.scale_log2, kMiddle);
+    }
 #pragma unroll
     for (int pass = 0; pass < kPasses; ++pass) {
       const int unit = pass * THREADS + threadIdx.x;
@@ -307,7 +358,7 @@ struct QueryRows {
       widen(raw[pass], a.q.dtype, x);
       put(x, up, unit / kRuns, unit % kRuns);
     }
-    return ldexpf(a.scale_log2, a.scale_exp + 24 - up);
+    return ldexpf(a.scale_log2, min(a.scale_exp + 24 - up, kMost));
   }
 };
 
@@ -416,7 +467,7 @@ struct Wave {
   static constexpr int kSlices = D / 32, kTiles = D / 16, kGroups = D / G;
   static constexpr float kHalf = BITS == 4 ? 8.0f : 128.0f;
   f16x8 q[NT][kSlices];          // query rows as matrix operands
-  float qs[NT][kGroups];         // sum of a row's q over a group, in log2 units of score
+  float qs[NT][kGroups];         // sum of a row's q over a group, in log2 units of score (over the row's factor)
   int lo[NT], hi[NT];            // visible keys: j <= hi and (j >= lo or j < sinks)
   f32x4 o[NT][kTiles];           // sum of p step einv (c - kHalf) 2^-9
   f32x4 st[NT];                  // rows: g: sum p zero; kGroups + g: sum p step; 2 kGroups: sum p
@@ -424,12 +475,22 @@ struct Wave {
   float mb[NT];                  // running maximum (log2) - kPeak
   bool none[NT];                 // no key seen yet
   bool fresh;                    // `none` of some row of the wave
+  // Rows have factors of their own (QueryRows::stage): scores then come without
+  // the running maximum, times 1 / factor, and are put right where masks are set,
+  // in a branch that steps of ordinary queries inside every row's view pass by
+  // (2048 rows after 16384 keys, and ragged prompts at 64 elements: 667 and 335 us;
+  // with one power of two for a block, which took bits from its smaller rows, 661
+  // and 331; with the maximum in each row's own units 664 and 346; with a walk over
+  // the keys for every range of sizes 697 and 368).
+  bool uneven;
+  const float* factor;           // of the wave's rows, in LDS
   float einv;                    // of o
 
-  // Rows row0 + first .. of the block's staged rows; rf: from raw scores to log2 units.
+  // Rows row0 + first .. of the block's staged rows; rf: from raw scores to log2
+  // units, but for the rows' own factors where they have some.
   template <int ROWS>
   __device__ __forceinline__ void begin(const KvAttnArgs& a, const Seq& sq, const QueryRows<BITS, D, G, ROWS>& from,
-                                        float rf, int row0, int first, int rows) {
+                                        float rf, bool own_factors, const float* factors, int row0, int first, int rows) {
     const int n = threadIdx.x % 16, lane = threadIdx.x % 64;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -450,6 +511,8 @@ struct Wave {
       none[t] = true;
     }
     fresh = true;
+    uneven = own_factors;
+    factor = factors + first;
     einv = 1.0f;
   }
 
@@ -466,14 +529,17 @@ struct Wave {
 
   // SUB tiles of 32 keys, at tokens tb.  key(u, s, w): operand of slice w of half
   // s of tile u; value(u, i): operand of value tile i; params(u): the tile's
-  // parameters; whole: every row sees all of the keys; ok: bit s: half s lies in
-  // a page of the cache.
+  // parameters; whole: every row sees all of the keys, and rows have no
+  // factors of their own; ok: bit s: half s lies in a page of the cache.
   template <int SUB, typename Key, typename Value, typename P>
   __device__ __forceinline__ void step(Key&& key, Value&& value, P&& params, const int (&tb)[SUB], bool whole, int len,
                                        const uint32_t (&ok)[SUB], int sinks) {
     const int lane = threadIdx.x % 64, quad = lane / 16;
-    // scores, in log2 units less the running maximum; half h % 2 of tile h / 2
+    // scores in log2 units less the running maximum; half h % 2 of tile h / 2
     float y[SUB][NT][2][4];
+    float less[NT];   // what scores come without
+#pragma unroll
+    for (int i = 0; i < NT; ++i) less[i] = uneven ? 0.0f : mb[i];
     constexpr int kHalves = 2 * SUB;
     constexpr Ahead kAhead = SUB > 1 ? ahead(D, G) : Ahead::kNothing;
     f16x8 ops[2][kSlices];
@@ -497,7 +563,7 @@ struct Wave {
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          const float z = fmaf(kz[h % 2][g][j], qs[i][g], g == 0 ? -mb[i] : y[h / 2][i][h % 2][j]);
+          const float z = fmaf(kz[h % 2][g][j], qs[i][g], g == 0 ? -less[i] : y[h / 2][i][h % 2][j]);
           y[h / 2][i][h % 2][j] = fmaf(ks[h % 2][g][j], acc[h % 2][g][i][j], z);
         }
     };
@@ -529,6 +595,18 @@ struct Wave {
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) scores(kHalves - 1, g);
     if (!whole) {
+      if (uneven) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const float f = factor[i * 16 + lane % 16];
+#pragma unroll
+          for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y[u][i][s][j] = fmaf(y[u][i][s][j], f, -mb[i]);
+        }
+      }
 #pragma unroll
       for (int u = 0; u < SUB; ++u)
 #pragma unroll
@@ -793,7 +871,8 @@ template <int BITS, int D, int G, int NT, int NW>
 struct FewLds {
   static constexpr int kRows = NT * 16, kStride = D + 4;
   QueryRows<BITS, D, G, kRows> q;
-  float top[NW];
+  float top[2 * NW];
+  float factor[kRows];
   float m[NW][kRows], l[NW][kRows];
   union {
     TileParams<D, G> params;    // in the wave's loop
@@ -836,17 +915,18 @@ __global__ __launch_bounds__(NW * 64, few_min_waves(BITS, D, G, NT)) void k_kv_a
   }
   TileParams<D, G>& params = lds.wave[wave].params;
   params.clear(threadIdx.x % 64);
-  const float rf = lds.q.template stage_together<NW * 64>(a, k.sq, k.hk, k.row0, k.rows, lds.top);
+  bool uneven;
+  const float rf = lds.q.template stage<NW * 64>(a, k.sq, k.hk, k.row0, k.rows, lds.top, lds.factor, uneven);
   __syncthreads();
   W w;
-  w.begin(a, k.sq, lds.q, rf, k.row0, 0, k.rows);
+  w.begin(a, k.sq, lds.q, rf, uneven, lds.factor, k.row0, 0, k.rows);
   StepScale scale;
   const Bounds r = bounds_of(a, k, k.row0, min(k.row0 + Lds::kRows, k.rows) - 1);
   auto work = [&](const Tile<BITS, D, G>& from, ParamWords<D, G>& words, uint32_t page_ok) {
     const int tb[1] = {k.span.token(t)};
     if (tile_seen(r, tb[0], a.sinks)) {
       const uint32_t ok[1] = {page_ok};
-      const bool whole = tile_whole(r, tb[0], k.sq.len, page_ok, a.sinks);
+      const bool whole = !uneven && tile_whole(r, tb[0], k.sq.len, page_ok, a.sinks);
       if (!whole) words.clear_unseen(tb[0], k.span.end, r.lo_min, a.sinks, page_ok);
       if (scale.see(words.largest_step())) w.set_scale(scale.einv);
       wave_sync();
@@ -920,8 +1000,8 @@ __global__ __launch_bounds__(NW * 64, few_min_waves(BITS, D, G, NT)) void k_kv_a
 // of one tile, into matrix operands in LDS (two buffers, one barrier a step),
 // and one wave the parameters into what the softmax uses; doing either per wave
 // would cost as much as the softmax.  The block's query rows share one power of
-// two, so that a score in log2 units less the running maximum takes two
-// multiply-adds: a key's step and the row factor are one number.
+// two (where their sizes allow it), so that a score in log2 units less the running
+// maximum takes two multiply-adds: a key's step and the row factor are one number.
 template <int BITS, int D, int G>
 struct ManyTile {
   f16x8 k[2][D / 32][64];
@@ -937,7 +1017,8 @@ struct ManyLds {
     float einv;                         // of the values' steps
     uint32_t ok[kSub];                  // bit s: half s lies in a page of the cache
   };
-  float top[NW];
+  float top[2 * NW];
+  float factor[kRows];
   union {
     QueryRows<BITS, D, G, kRows> q;     // before the first step
     Step step[2];
@@ -1005,10 +1086,11 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void k_kv_attention_many(
   const int lane = threadIdx.x % 64, n = lane % 16, quad = lane / 16;
   const int first = wave * NT * 16;
 
-  const float rf = lds.q.template stage_together<NW * 64>(a, k.sq, k.hk, k.row0, k.rows, lds.top);
+  bool uneven;
+  const float rf = lds.q.template stage<NW * 64>(a, k.sq, k.hk, k.row0, k.rows, lds.top, lds.factor, uneven);
   __syncthreads();
   W w;
-  w.begin(a, k.sq, lds.q, rf, k.row0, first, k.rows);
+  w.begin(a, k.sq, lds.q, rf, uneven, lds.factor, k.row0, first, k.rows);
   __syncthreads();             // the steps overwrite the staged rows
   for (int i = threadIdx.x; i < 2 * SUB * 64; i += NW * 64)
     lds.step[i / (SUB * 64)].tile[i / 64 % SUB].params.clear(i % 64);
@@ -1089,7 +1171,7 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void k_kv_attention_many(
         auto uniform = [](uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); };
         w.set_scale(__uint_as_float(uniform(__float_as_uint(now.einv))));
         const uint32_t ok_now[SUB] = {uniform(now.ok[0]), uniform(now.ok[1])};
-        const bool whole = tile_whole(r, tb[0], k.sq.len, ok_now[0], a.sinks) &&
+        const bool whole = !uneven && tile_whole(r, tb[0], k.sq.len, ok_now[0], a.sinks) &&
                            tile_whole(r, tb[1], k.sq.len, ok_now[1], a.sinks);
         w.template step<SUB>([&](int u, int s, int i) { return now.tile[u].k[s][i][lane]; },
                              [&](int u, int i) { return now.tile[u].v[i][lane]; },

@@ -38,6 +38,58 @@ def check(s, out, q, n, rows=None, **kw):
     s.check(out[rows], q[rows], 0, s.lens[0] - n + rows, s.lens[0], **kw)
 
 
+@pytest.mark.parametrize("far", [12, 20, 30, 60, 100])
+@pytest.mark.parametrize("n", [3, 40])                       # few rows of a K/V head, many
+@pytest.mark.parametrize("D,bits,group", FORMS)
+def test_rows_of_very_different_size(D, bits, group, n, far):
+    """One token, then one head, 2^far times larger than the others: those keep their bits."""
+    for what in ("token", "head", "small"):
+        s, q = filled(n, D, bits, group, seed=far)
+        if what == "token":
+            q[1] *= 2.0 ** far
+        elif what == "head":
+            q[:, 2] *= 2.0 ** far
+        else:
+            q[1:] *= 2.0 ** -far
+        check(s, run(s, q, n), q, n)
+
+
+@pytest.mark.parametrize("n", [3, 40])
+@pytest.mark.parametrize("D,bits,group", FORMS)
+def test_half_precision_rows_of_very_different_size(D, bits, group, n):
+    s, q = filled(n, D, bits, group, dtype="f16", seed=1)
+    q[1] *= 2.0 ** 13
+    q[2] *= 2.0 ** -13
+    check(s, run(s, q, n), q, n)
+
+
+@pytest.mark.parametrize("n", [3, 40])
+@pytest.mark.parametrize("top", [2.0 ** 119, 2.0 ** 123, 2.0 ** 126, 2.0 ** 127])
+def test_the_largest_queries_leave_the_other_rows(n, top):
+    """A row near the end of bf16's range whose own scores fit binary32 (a single large element)."""
+    s, q = filled(n, seed=2)
+    q[1] = 0
+    q[1, :, 5] = top
+    out = run(s, q, n)
+    check(s, out, q, n, [i for i in range(n) if i != 1])
+    assert out[1].isfinite().all()
+
+
+@pytest.mark.parametrize("n", [3, 40])
+def test_all_rows_near_the_end_of_the_range(n):
+    """One key holds all the weight; its values come back."""
+    s, q = filled(n, seed=3)
+    q[:] = 0
+    q[:, :, 5] = 2.0 ** 126
+    out = U.host64(run(s, q, n))
+    k, v = (U.values(*U.quantize(U.host64(x), 4, 128), 128) for x in s.kv[0])
+    for i in range(n):
+        for h in range(s.heads * s.per):
+            want = v[np.argmax(k[:150 - n + i + 1, h // s.per, 5]), h // s.per]
+            # one probability and its product with the step round to f16, the output to bf16
+            assert (np.abs(out[i, h] - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * np.abs(v).max()).all()
+
+
 @pytest.mark.parametrize("n", [3, 40])
 @pytest.mark.parametrize("far", range(16, 44))
 def test_scores_of_every_size(n, far):
