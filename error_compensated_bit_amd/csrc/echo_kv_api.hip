@@ -11,7 +11,7 @@ using namespace echo;
 
 namespace {
 
-constexpr int64_t kMaxBlocks = 0xffffffffll / 256;   // a dispatch holds at most 2^32 - 1 work-items
+constexpr int64_t kMaxThreads = 0xffffffffll;        // work-items of a dispatch along x
 constexpr int64_t kMaxSeqs = 65535;
 constexpr int32_t kMaxRows = 1 << 30;                // row and position indices stay inside 31 bits
 
@@ -133,7 +133,8 @@ int check_attention(const echo_kv_cache* c, const echo_kv_batch* b, int q_heads,
   const KvBatch k = batch_of(b);
   if ((int64_t)k.max_new * per > (int64_t)1 << 30) return ECHO_ERR_SHAPE;
   *plan = kv_attention_plan(cache_of(c), k, per, causal, window, sinks);
-  if ((int64_t)c->kv_heads * b->seqs * plan->row_blocks > kMaxBlocks / plan->splits) return ECHO_ERR_SHAPE;
+  const int64_t most = kMaxThreads / kv_plan_threads(*plan) / plan->splits;
+  if ((int64_t)c->kv_heads * b->seqs * plan->row_blocks > most) return ECHO_ERR_SHAPE;
   return ECHO_OK;
 }
 
@@ -153,7 +154,7 @@ int cache_rows(const echo_kv_cache* cache, const echo_kv_batch* batch, const ech
   if ((rc = check_form(cache)) || (rc = check_batch_sizes(batch))) return rc;
   if (!k || !v) return ECHO_ERR_ARG;
   if (k->dtype != v->dtype) return ECHO_ERR_ARG;
-  if (kv_cache_blocks(cache_of(cache), batch_of(batch)) > kMaxBlocks) return ECHO_ERR_SHAPE;
+  if (kv_cache_blocks(cache_of(cache), batch_of(batch)) > kMaxThreads / kKvCacheThreads) return ECHO_ERR_SHAPE;
   if (batch->rows == 0 || batch->seqs == 0) return ECHO_OK;
   if ((rc = check_cache(cache)) || (rc = check_batch(batch))) return rc;
   if ((rc = check_rows(k, batch->rows, cache->kv_heads, cache->head_dim, true, out))) return rc;

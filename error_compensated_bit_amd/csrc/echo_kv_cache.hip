@@ -19,7 +19,7 @@
 namespace echo {
 namespace kv {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kKvCacheThreads;
 
 // One step of a minimum and a maximum between lanes.  Written out because the
 // compiler keeps the move between lanes apart from the minimum and quiets its

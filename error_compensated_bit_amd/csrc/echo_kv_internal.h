@@ -71,7 +71,8 @@ struct KvAttnArgs {
 // Each returns the first launch error (hipSuccess when every launch went out).
 hipError_t run_kv_write(const KvWriteArgs& a, hipStream_t st);
 hipError_t run_kv_read(const KvWriteArgs& a, hipStream_t st);
-// Blocks along x of both.
+// Blocks along x of both, and their threads.
+constexpr int kKvCacheThreads = 256;
 int64_t kv_cache_blocks(const KvCache& c, const KvBatch& b);
 hipError_t run_kv_attention(const KvAttnArgs& a, hipStream_t st);
 
@@ -83,6 +84,8 @@ hipError_t run_kv_attention_form(const KvAttnArgs& a, hipStream_t st);
 constexpr int kv_many_tiles(int head_dim) { return head_dim == 256 ? 1 : 2; }
 constexpr int kv_many_waves(int head_dim) { return head_dim == 64 ? 4 : 8; }
 KvPlan kv_attention_plan(const KvCache& c, const KvBatch& b, int heads_per_kv, int causal, int window, int sinks);
+// Threads of a block.
+inline int kv_plan_threads(const KvPlan& p) { return 64 * (p.row_waves == 1 ? p.key_waves : p.row_waves); }
 // Rows of one (sequence, K/V head) in the partial results.
 int64_t kv_plan_rows(const KvPlan& p);
 

@@ -1,0 +1,19 @@
+"""Limits of the quantized K/V cache calls without a GPU: sizes just past what a
+dispatch holds or 64-bit offsets reach are refused by the host."""
+import pytest
+
+from error_compensated_bit_amd import binding as B
+from test_kv_abi import attention, batch, cache, qrows, ref, rows
+
+
+# kv_heads * seqs * blocks of 256 rows (128 elements), 128 rows (256 elements and 64) of waves * 64 threads
+@pytest.mark.parametrize("head_dim,group,row_block,threads", [(128, 128, 256, 512), (256, 128, 128, 512), (64, 64, 128, 256)])
+def test_attention_grids(head_dim, group, row_block, threads):
+    L, seqs, heads, per = B.load_library(), 65535, 8, 4
+    most = (2 ** 32 - 1) // threads // (seqs * heads)           # blocks of rows that a dispatch holds
+    new = (most + 1) * row_block // per
+    form = dict(head_dim=head_dim, group=group, kv_heads=heads)
+    b = batch(seqs=seqs, rows=new, max_new=new, max_len=64)
+    stride = dict(row_stride=heads * per * head_dim, head_stride=head_dim)
+    assert attention(L, c=cache(**form), b=b, heads=heads * per, q=qrows(**stride), out=qrows(**stride)) == B.ECHO_ERR_SHAPE
+    assert L.echo_kv_workspace_bytes(cache(**form), b, heads * per, 1, 0, 0) == 0
