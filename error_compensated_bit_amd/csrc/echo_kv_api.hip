@@ -71,16 +71,16 @@ int check_rows(const echo_kv_rows* r, int64_t rows, int64_t heads, int64_t D, bo
   if (!r) return ECHO_ERR_ARG;
   if (r->dtype != ECHO_KV_BF16 && r->dtype != ECHO_KV_F16 && !(f32 && r->dtype == ECHO_KV_F32)) return ECHO_ERR_ARG;
   if ((rc = check_buf(r->data))) return rc;
-  const int64_t most = (int64_t)1 << 40;    // (rows - 1) * stride cannot overflow
-  if (r->row_stride < 0 || r->head_stride < 0 || r->row_stride > most || r->head_stride > most) return ECHO_ERR_ARG;
+  const int64_t rs = r->row_stride, hs = r->head_stride;
+  const int64_t most = (int64_t)1 << 40;    // elements from the first row to the last one, more than any memory
+  if (rs < 0 || hs < 0 || rs > most || hs > most) return ECHO_ERR_ARG;
+  if ((rows > 1 && rs > most / (rows - 1)) || (heads > 1 && hs > most / (heads - 1))) return ECHO_ERR_ARG;
   const int64_t unit = r->dtype == ECHO_KV_F32 ? 4 : 8;
-  if ((rows > 1 && r->row_stride % unit) || (heads > 1 && r->head_stride % unit)) return ECHO_ERR_ALIGN;
+  if ((rows > 1 && rs % unit) || (heads > 1 && hs % unit)) return ECHO_ERR_ALIGN;
   if (out) {
-    // (rows - 1) * stride stays below 2^21 * 2^42 for every stride that can matter here
-    const int64_t rs = r->row_stride, hs = r->head_stride;
+    // (rows - 1) * rs and (heads - 1) * hs are at most `most` each
     const bool row_major = (heads == 1 || hs >= D) && (rows == 1 || rs >= (heads - 1) * hs + D);
-    const bool head_major = (rows == 1 || rs >= D) &&
-                            (heads == 1 || (rs <= (most - D) / (rows > 1 ? rows - 1 : 1) && hs >= (rows - 1) * rs + D));
+    const bool head_major = (rows == 1 || rs >= D) && (heads == 1 || hs >= (rows - 1) * rs + D);
     if (!row_major && !head_major) return ECHO_ERR_ARG;
   }
   return ECHO_OK;

@@ -17,3 +17,20 @@ def test_attention_grids(head_dim, group, row_block, threads):
     stride = dict(row_stride=heads * per * head_dim, head_stride=head_dim)
     assert attention(L, c=cache(**form), b=b, heads=heads * per, q=qrows(**stride), out=qrows(**stride)) == B.ECHO_ERR_SHAPE
     assert L.echo_kv_workspace_bytes(cache(**form), b, heads * per, 1, 0, 0) == 0
+
+
+@pytest.mark.parametrize("fault", [dict(row_stride=1 << 40), dict(row_stride=1 << 20), dict(row_stride=4096),
+                                   dict(head_stride=1 << 40)])
+def test_arrays_larger_than_any_memory(fault):
+    """Strides whose product with the rows or heads passes 2^40 elements, and at
+    the far end 64 bits of bytes."""
+    L = B.load_library()
+    form = dict(kv_heads=4, head_dim=128)
+    b = batch(seqs=1, rows=1 << 29, max_new=64, max_len=64)
+    stride = {**dict(row_stride=1024, head_stride=128), **fault}
+    small = batch(seqs=1, rows=64, max_new=64, max_len=64)
+    for call in (L.echo_kv_write, L.echo_kv_read):
+        assert call(cache(**form), b, rows(**stride), rows(**stride), None) == B.ECHO_ERR_ARG
+    assert attention(L, c=cache(**form), b=b, heads=4, q=qrows(**stride), out=qrows(row_stride=512)) == B.ECHO_ERR_ARG
+    if "row_stride" in fault and fault["row_stride"] == 1 << 40:
+        assert L.echo_kv_write(cache(**form), small, rows(**stride), rows(**stride), None) == B.ECHO_ERR_ARG
