@@ -159,6 +159,7 @@ int cache_rows(const echo_kv_cache* cache, const echo_kv_batch* batch, const ech
   if ((rc = check_cache(cache)) || (rc = check_batch(batch))) return rc;
   if ((rc = check_rows(k, batch->rows, cache->kv_heads, cache->head_dim, true, out))) return rc;
   if ((rc = check_rows(v, batch->rows, cache->kv_heads, cache->head_dim, true, out))) return rc;
+  if (out && k->data == v->data) return ECHO_ERR_ARG;
   a->c = cache_of(cache);
   a->b = batch_of(batch);
   a->k = rows_of(k);

@@ -243,7 +243,8 @@ typedef struct echo_kv_batch {
 } echo_kv_batch;
 
 /* Packed rows [rows, heads, head_dim], head_dim contiguous, strides in elements.
- * Every row is 16-byte aligned; rows that are written share no element. */
+ * Every row is 16-byte aligned, strides reach 2^40 elements at most; rows that
+ * are written share no element. */
 #define ECHO_KV_BF16     0
 #define ECHO_KV_F16      1
 #define ECHO_KV_F32      2
@@ -266,7 +267,8 @@ int echo_kv_write(const echo_kv_cache* cache, const echo_kv_batch* batch,
 
 /*
  * echo_kv_read -- the batch's rows of keys and values as bf16, fp16 (rounded to
- *   nearest even) or fp32.  Rows the call passes over keep their contents.
+ *   nearest even) or fp32.  Rows the call passes over keep their contents.  k
+ *   and v share no element (the same array twice is ECHO_ERR_ARG).
  *   Errors: ECHO_ERR_ARG, ECHO_ERR_SHAPE, ECHO_ERR_ALIGN, ECHO_ERR_HIP.
  */
 int echo_kv_read(const echo_kv_cache* cache, const echo_kv_batch* batch,

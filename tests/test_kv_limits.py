@@ -34,3 +34,10 @@ def test_arrays_larger_than_any_memory(fault):
     assert attention(L, c=cache(**form), b=b, heads=4, q=qrows(**stride), out=qrows(row_stride=512)) == B.ECHO_ERR_ARG
     if "row_stride" in fault and fault["row_stride"] == 1 << 40:
         assert L.echo_kv_write(cache(**form), small, rows(**stride), rows(**stride), None) == B.ECHO_ERR_ARG
+
+
+def test_reading_keys_and_values_into_one_array():
+    """Two results in the same place would leave either: refused.  Writing both from one array is fine."""
+    L = B.load_library()
+    assert L.echo_kv_read(cache(), batch(), rows(), rows(), None) == B.ECHO_ERR_ARG
+    assert L.echo_kv_read(cache(), batch(), rows(), rows(data=0x10000 + 8), None) == B.ECHO_ERR_ALIGN
