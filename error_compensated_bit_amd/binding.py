@@ -225,8 +225,10 @@ class Prepared:
     payload tables, pointers and stream): calling it makes only the foreign
     call.  For callers that repeat the same call on the same buffers, where
     marshalling would cost more host time than a small message's kernels.
-    It holds references to every tensor it was given, so they stay allocated
-    while it exists; it always launches on the stream it was prepared with."""
+    It holds references to every tensor it was given (the tensors themselves:
+    a payload, cache or batch may be given others afterwards), so they stay
+    allocated while it exists; it always launches on the stream it was prepared
+    with."""
 
     def __init__(self, fn, args, keep, where: str):
         self._fn = fn
@@ -240,13 +242,18 @@ class Prepared:
             raise EchoError(rc, self._where)
 
 
+def _tensors(*owners) -> list:
+    """The tensors that payloads, caches and batches hold now."""
+    return [t for o in owners if o is not None for t in vars(o).values() if isinstance(t, torch.Tensor)]
+
+
 def prepare_quantize_feedback(cfg: echo_config, P: int, rank: int, n: int, x: torch.Tensor,
                               state: torch.Tensor, out, stream=None) -> Prepared:
     L = load_library()
     c = echo_config(*(getattr(cfg, f) for f, _ in echo_config._fields_))
     return Prepared(L.echo_quantize_feedback,
                     (ctypes.byref(c), P, rank, n, _ptr(x), _ptr(state), _seg_table(P, out),
-                     _stream(stream)), (c, x, state, list(out)), "echo_quantize_feedback")
+                     _stream(stream)), (c, x, state, _tensors(*out)), "echo_quantize_feedback")
 
 
 def prepare_owner_reduce_requant(cfg: echo_config, P: int, rank: int, n: int, x: torch.Tensor,
@@ -256,7 +263,7 @@ def prepare_owner_reduce_requant(cfg: echo_config, P: int, rank: int, n: int, x:
     out_seg = out.seg()
     return Prepared(L.echo_owner_reduce_requant,
                     (ctypes.byref(c), P, rank, n, _ptr(x), _ptr(state), _seg_table(P, inp),
-                     ctypes.byref(out_seg), _stream(stream)), (c, out_seg, x, state, list(inp), out),
+                     ctypes.byref(out_seg), _stream(stream)), (c, out_seg, x, state, _tensors(*inp, out)),
                     "echo_owner_reduce_requant")
 
 
@@ -266,7 +273,7 @@ def prepare_dequant_gather(cfg: echo_config, P: int, n: int, inp, out: torch.Ten
     c = echo_config(*(getattr(cfg, f) for f, _ in echo_config._fields_))
     return Prepared(L.echo_dequant_gather,
                     (ctypes.byref(c), P, n, _seg_table(P, inp), _ptr(out), _stream(stream)),
-                    (c, list(inp), out), "echo_dequant_gather")
+                    (c, _tensors(*inp), out), "echo_dequant_gather")
 
 
 # ------------------------------------------------------------------ quantized K/V cache
@@ -407,7 +414,7 @@ def _prepare_kv_rows(fn, where: str, cache: KVCache, batch: KVBatch, k, v, strea
     device, c, b, st = _kv_call(cache, batch, stream)
     kr, vr = (_kv_rows(t, n, batch.rows, cache.kv_heads, cache.head_dim, device) for t, n in ((k, "k"), (v, "v")))
     return _PreparedOn(fn, (ctypes.byref(c), ctypes.byref(b), ctypes.byref(kr), ctypes.byref(vr), st),
-                       (c, b, kr, vr, cache, batch, k, v), where, device)
+                       (c, b, kr, vr, _tensors(cache, batch), k, v), where, device)
 
 
 def prepare_kv_write(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream=None) -> Prepared:
@@ -443,7 +450,7 @@ def prepare_kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, out: t
     return _PreparedOn(load_library().echo_kv_attention,
                        (ctypes.byref(c), ctypes.byref(b), q_heads, ctypes.byref(qr), ctypes.byref(outr), scale,
                         int(causal), window, sinks, _ptr(workspace) or None, workspace.numel(), st),
-                       (c, b, qr, outr, cache, batch, q, out, workspace), "echo_kv_attention", device)
+                       (c, b, qr, outr, _tensors(cache, batch), q, out, workspace), "echo_kv_attention", device)
 
 
 def echo_kv_write(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream=None):
