@@ -277,6 +277,14 @@ def prepare_dequant_gather(cfg: echo_config, P: int, n: int, inp, out: torch.Ten
 
 
 # ------------------------------------------------------------------ quantized K/V cache
+def _int(width: int, /, **values):
+    """Refuse what a signed integer of that width does not hold: ctypes would
+    pass its lower bits."""
+    for name, v in values.items():
+        if not -(1 << width - 1) <= v < 1 << width - 1:
+            raise ValueError(f"{name}: {v} does not fit {width} bits")
+
+
 _KV_DTYPES = {torch.bfloat16: ECHO_KV_BF16, torch.float16: ECHO_KV_F16, torch.float32: ECHO_KV_F32}
 
 
@@ -322,6 +330,7 @@ class KVCache:
                                  f"got {t.dtype} {tuple(t.shape)} on {t.device}")
             if not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
+        _int(32, bits=self.bits, group=self.group, head_dim=self.head_dim)
         return echo_kv_cache(self.bits, self.group, self.head_dim, heads, slots, 0, pages, _ptr(self.k_codes),
                              _ptr(self.v_codes), _ptr(self.k_params), _ptr(self.v_params))
 
@@ -347,11 +356,14 @@ class KVBatch:
         for t in (self.row_start, self.kv_len, self.page_table):
             if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
                 raise ValueError(f"a batch's arrays are contiguous int32 on the cache's device {device}")
+        _int(32, rows=self.rows, max_new=self.max_new, max_len=self.max_len)
         return echo_kv_batch(seqs, self.rows, self.max_new, self.max_len, self.page_table.shape[1],
                              _ptr(self.row_start), _ptr(self.kv_len), _ptr(self.page_table))
 
 
 def _kv_form(num_pages, page_size, kv_heads, head_dim, bits, group) -> echo_kv_cache:
+    _int(32, bits=bits, group=group, head_dim=head_dim, kv_heads=kv_heads, page_size=page_size)
+    _int(64, num_pages=num_pages)
     return echo_kv_cache(bits, group, head_dim, kv_heads, page_size, 0, num_pages, None, None, None, None)
 
 
@@ -428,6 +440,7 @@ def prepare_kv_read(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Te
 def echo_kv_workspace_bytes(cache: KVCache, batch: KVBatch, q_heads: int, causal=True, window: int = 0,
                             sinks: int = 0) -> int:
     c, b = cache.desc(), batch.desc(cache.device)
+    _int(32, q_heads=q_heads, window=window, sinks=sinks)
     return load_library().echo_kv_workspace_bytes(ctypes.byref(c), ctypes.byref(b), q_heads, int(causal), window,
                                                   sinks)
 
@@ -439,6 +452,7 @@ def prepare_kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, out: t
     of the prepared call's own.  Calls that may run at the same time (other
     streams, graphs replayed side by side) must not share one."""
     device, c, b, st = _kv_call(cache, batch, stream)
+    _int(32, window=window, sinks=sinks)
     q_heads = q.shape[1] if q.dim() == 3 else 0
     qr, outr = (_kv_rows(t, n, batch.rows, q_heads, cache.head_dim, device) for t, n in ((q, "q"), (out, "out")))
     if workspace is None:
