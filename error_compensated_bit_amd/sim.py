@@ -116,7 +116,8 @@ def attention_site(cfg, r: Ranks, a: AttentionRanks, batch: B.KVBatch, qs, ks, v
     """One attention site on the current stream: every rank writes its heads'
     new keys and values, attends over its cache and multiplies with its rows of
     the output projection; the partial products are summed by one call.
-    qs, ks, vs: the ranks' projected rows [batch.rows, heads, head_dim];
+    qs, ks, vs: the ranks' projected rows [batch.rows, heads, head_dim]; rows of
+    no sequence (padding, or past max_new) bring nothing into the sum;
     r: ranks with messages of batch.rows * hidden elements."""
     if r.n != batch.rows * a.projections[0].shape[1] or not r.P == len(a.caches) == len(qs) == len(ks) == len(vs):
         raise ValueError(f"{batch.rows} rows of {a.projections[0].shape[1]} from {len(a.caches)} ranks do not make "
@@ -126,6 +127,7 @@ def attention_site(cfg, r: Ranks, a: AttentionRanks, batch: B.KVBatch, qs, ks, v
     for p in range(r.P):
         att, part = a.attended[p][:batch.rows], a.partial[p][:batch.rows]
         B.echo_kv_write(a.caches[p], batch, ks[p], vs[p])
+        att.zero_()   # rows of no sequence keep their contents, and would reach the message and the error state
         B.echo_kv_attention(a.caches[p], batch, qs[p], att, scale, workspace=a.workspace)
         torch.mm(att.flatten(1), a.projections[p], out=part)
     return allreduce(cfg, r, [a.partial[p][:batch.rows].reshape(-1) for p in range(r.P)])
