@@ -798,7 +798,12 @@ __device__ __forceinline__ void store_out8(const KvRows& out, int64_t e, const f
 // not coherent: they are stored and loaded as agent-scope atomics, which go
 // through to the common memory.  (Fences of that scope write back and drop the
 // whole L2 instead: with one per block a decode step of 64 sequences took 150
-// us in place of 46.)
+// us in place of 46.)  Their order against the arrival counter is gfx950's, not
+// the language's, which orders no relaxed atomics: an agent-scope store (sc1) has
+// left the die's L2 when vmcnt counts it down, so behind s_waitcnt vmcnt(0) of
+// every wave, and the barrier, the counter is only reached by results that are
+// there for all dies; and an agent-scope load (sc1) takes no older line from its
+// own L2.
 __device__ __forceinline__ void put_shared(float* p, float v) {
   __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -880,7 +885,12 @@ struct FewLds {
   } wave[NW];
 };
 
-// Waves per SIMD that the registers leave room for without spilling.
+// Waves per SIMD that the registers leave room for.  With 8 waves a block there
+// are two at least, and then groups of 32 spill: 1 register at 4 bits, 128
+// elements and two tiles, 45 at 4 bits and 256 elements, 46 at 8 bits, 128
+// elements and two tiles.  64 sequences of 4096 keys, groups of 32 / 128: 83 / 62,
+// 162 / 103 (one row of 4 heads) and 147 / 104 us; without spills, at 4 bits, 128
+// elements and one tile, 66 / 56.
 constexpr int few_min_waves(int BITS, int D, int G, int NT) {
   if (NT == 1) return D == 64 ? (BITS * (64 / G) > 8 ? 3 : 4) : D == 128 ? (BITS == 4 && G > 32 ? 3 : 2) : BITS == 4 && G > 32 ? 2 : 1;
   return BITS * (128 / G) < 32 ? 2 : 1;

@@ -277,13 +277,15 @@ int echo_kv_read(const echo_kv_cache* cache, const echo_kv_batch* batch,
 /*
  * echo_kv_attention -- out = softmax(scale * q K^T) V over the cache.
  *   q, out: [rows, q_heads, head_dim], both bf16 or both fp16; query head h
- *   reads K/V head h / (q_heads / kv_heads).  The row at position p sees the
- *   keys j < kv_len[b]; with causal = 1 only j <= p; with window > 0 (causal
- *   only) of these only p - j < window or j < sinks.  A row that sees nothing
- *   becomes 0.  scale: finite.
- *   Scores, the softmax and sums are binary32 on the unrounded cached values;
- *   probabilities enter the second product in fp16, relative to the row's
- *   maximum.
+ *   reads K/V head h / (q_heads / kv_heads).  out may be q itself, else they
+ *   share no element.  The row at position p sees the keys j < kv_len[b]; with
+ *   causal = 1 only j <= p; with window > 0 (causal only) of these only
+ *   p - j < window or j < sinks.  Slots that no row sees may hold anything.  A row
+ *   that sees nothing becomes 0; one that sees something and has a NaN or infinite
+ *   query element, NaN.  scale: finite.
+ *   Scores, the softmax and sums are binary32 on the unrounded cached values; a
+ *   query element enters within 2^-25 of its row's largest finite one, and
+ *   probabilities enter the second product in fp16, relative to the row's maximum.
  *   workspace: echo_kv_workspace_bytes() bytes (may be NULL if that is 0), all 0
  *   when it is first used, and again after a call that failed with
  *   ECHO_ERR_HIP; a completed call leaves it ready for the next, of any sizes
