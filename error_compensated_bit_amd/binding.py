@@ -129,6 +129,9 @@ class Payload:
     codes: torch.Tensor
     params: torch.Tensor
 
+    def tensors(self) -> tuple:
+        return self.codes, self.params
+
     def seg(self) -> echo_seg:
         return echo_seg(_ptr(self.codes), _ptr(self.params))
 
@@ -242,18 +245,13 @@ class Prepared:
             raise EchoError(rc, self._where)
 
 
-def _tensors(*owners) -> list:
-    """The tensors that payloads, caches and batches hold now."""
-    return [t for o in owners if o is not None for t in vars(o).values() if isinstance(t, torch.Tensor)]
-
-
 def prepare_quantize_feedback(cfg: echo_config, P: int, rank: int, n: int, x: torch.Tensor,
                               state: torch.Tensor, out, stream=None) -> Prepared:
     L = load_library()
     c = echo_config(*(getattr(cfg, f) for f, _ in echo_config._fields_))
     return Prepared(L.echo_quantize_feedback,
                     (ctypes.byref(c), P, rank, n, _ptr(x), _ptr(state), _seg_table(P, out),
-                     _stream(stream)), (c, x, state, _tensors(*out)), "echo_quantize_feedback")
+                     _stream(stream)), (c, x, state, [p.tensors() for p in out if p]), "echo_quantize_feedback")
 
 
 def prepare_owner_reduce_requant(cfg: echo_config, P: int, rank: int, n: int, x: torch.Tensor,
@@ -263,7 +261,7 @@ def prepare_owner_reduce_requant(cfg: echo_config, P: int, rank: int, n: int, x:
     out_seg = out.seg()
     return Prepared(L.echo_owner_reduce_requant,
                     (ctypes.byref(c), P, rank, n, _ptr(x), _ptr(state), _seg_table(P, inp),
-                     ctypes.byref(out_seg), _stream(stream)), (c, out_seg, x, state, _tensors(*inp, out)),
+                     ctypes.byref(out_seg), _stream(stream)), (c, out_seg, x, state, [p.tensors() for p in (*inp, out) if p]),
                     "echo_owner_reduce_requant")
 
 
@@ -273,13 +271,16 @@ def prepare_dequant_gather(cfg: echo_config, P: int, n: int, inp, out: torch.Ten
     c = echo_config(*(getattr(cfg, f) for f, _ in echo_config._fields_))
     return Prepared(L.echo_dequant_gather,
                     (ctypes.byref(c), P, n, _seg_table(P, inp), _ptr(out), _stream(stream)),
-                    (c, _tensors(*inp), out), "echo_dequant_gather")
+                    (c, [p.tensors() for p in inp if p], out), "echo_dequant_gather")
 
 
 # ------------------------------------------------------------------ quantized K/V cache
+_INT32 = 1 << 31
+
+
 def _int(width: int, /, **values):
     """Refuse what a signed integer of that width does not hold: ctypes would
-    pass its lower bits."""
+    pass its lower bits.  (The calls of a step compare with _INT32 first.)"""
     for name, v in values.items():
         if not -(1 << width - 1) <= v < 1 << width - 1:
             raise ValueError(f"{name}: {v} does not fit {width} bits")
@@ -318,6 +319,9 @@ class KVCache:
     def device(self) -> torch.device:
         return self.k_codes.device
 
+    def tensors(self) -> tuple:
+        return self.k_codes, self.v_codes, self.k_params, self.v_params
+
     def desc(self) -> echo_kv_cache:
         pages, heads, slots = self.k_codes.shape[:3]
         want = {"codes": ((pages, heads, slots, self.head_dim * self.bits // 8), torch.uint8),
@@ -330,7 +334,8 @@ class KVCache:
                                  f"got {t.dtype} {tuple(t.shape)} on {t.device}")
             if not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
-        _int(32, bits=self.bits, group=self.group, head_dim=self.head_dim)
+        if max(self.bits, self.group, self.head_dim) >= _INT32 or min(self.bits, self.group, self.head_dim) < -_INT32:
+            _int(32, bits=self.bits, group=self.group, head_dim=self.head_dim)
         return echo_kv_cache(self.bits, self.group, self.head_dim, heads, slots, 0, pages, _ptr(self.k_codes),
                              _ptr(self.v_codes), _ptr(self.k_params), _ptr(self.v_params))
 
@@ -348,6 +353,9 @@ class KVBatch:
     max_new: int
     max_len: int
 
+    def tensors(self) -> tuple:
+        return self.row_start, self.kv_len, self.page_table
+
     def desc(self, device: torch.device) -> echo_kv_batch:
         seqs = self.kv_len.numel()
         if self.page_table.dim() != 2 or self.page_table.shape[0] != seqs or self.row_start.shape != (seqs + 1,) \
@@ -356,7 +364,8 @@ class KVBatch:
         for t in (self.row_start, self.kv_len, self.page_table):
             if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
                 raise ValueError(f"a batch's arrays are contiguous int32 on the cache's device {device}")
-        _int(32, rows=self.rows, max_new=self.max_new, max_len=self.max_len)
+        if max(self.rows, self.max_new, self.max_len) >= _INT32 or min(self.rows, self.max_new, self.max_len) < -_INT32:
+            _int(32, rows=self.rows, max_new=self.max_new, max_len=self.max_len)
         return echo_kv_batch(seqs, self.rows, self.max_new, self.max_len, self.page_table.shape[1],
                              _ptr(self.row_start), _ptr(self.kv_len), _ptr(self.page_table))
 
@@ -426,7 +435,7 @@ def _prepare_kv_rows(fn, where: str, cache: KVCache, batch: KVBatch, k, v, strea
     device, c, b, st = _kv_call(cache, batch, stream)
     kr, vr = (_kv_rows(t, n, batch.rows, cache.kv_heads, cache.head_dim, device) for t, n in ((k, "k"), (v, "v")))
     return _PreparedOn(fn, (ctypes.byref(c), ctypes.byref(b), ctypes.byref(kr), ctypes.byref(vr), st),
-                       (c, b, kr, vr, _tensors(cache, batch), k, v), where, device)
+                       (c, b, kr, vr, cache.tensors(), batch.tensors(), k, v), where, device)
 
 
 def prepare_kv_write(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream=None) -> Prepared:
@@ -452,19 +461,21 @@ def prepare_kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, out: t
     of the prepared call's own.  Calls that may run at the same time (other
     streams, graphs replayed side by side) must not share one."""
     device, c, b, st = _kv_call(cache, batch, stream)
-    _int(32, window=window, sinks=sinks)
+    if max(window, sinks) >= _INT32 or min(window, sinks) < -_INT32:
+        _int(32, window=window, sinks=sinks)
     q_heads = q.shape[1] if q.dim() == 3 else 0
     qr, outr = (_kv_rows(t, n, batch.rows, q_heads, cache.head_dim, device) for t, n in ((q, "q"), (out, "out")))
     if workspace is None:
         with torch.cuda.stream(_as_stream(device, stream)):
-            workspace = torch.zeros(echo_kv_workspace_bytes(cache, batch, q_heads, causal, window, sinks),
-                                    dtype=torch.uint8, device=device)
+            room = load_library().echo_kv_workspace_bytes(ctypes.byref(c), ctypes.byref(b), q_heads, int(causal), window,
+                                                          sinks)
+            workspace = torch.zeros(room, dtype=torch.uint8, device=device)
     elif workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace: contiguous uint8 on {device}")
     return _PreparedOn(load_library().echo_kv_attention,
                        (ctypes.byref(c), ctypes.byref(b), q_heads, ctypes.byref(qr), ctypes.byref(outr), scale,
                         int(causal), window, sinks, _ptr(workspace) or None, workspace.numel(), st),
-                       (c, b, qr, outr, _tensors(cache, batch), q, out, workspace), "echo_kv_attention", device)
+                       (c, b, qr, outr, cache.tensors(), batch.tensors(), q, out, workspace), "echo_kv_attention", device)
 
 
 def echo_kv_write(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream=None):
