@@ -35,7 +35,7 @@
 // Measured (bf16, 4 bits in groups of 128, 32 query and 8 K/V heads of 128
 // elements): one new token of 4 sequences of about 126000 keys 106 us, 5.2 TB/s;
 // of 64 sequences of 1100 to 4100 keys 45 us, 4.1 TB/s (the longest sequence's
-// block is the whole time); 2048 new tokens after 16384 661 us, 884 TFLOP/s.
+// block is the whole time); 2048 new tokens after 16384 670 us, 872 TFLOP/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
