@@ -22,6 +22,7 @@ def attend_at(q, pos, k, v, causal, window, sinks, scale, spread, there=None):
     n, Hq, D = q.shape
     length, Hk = k.shape[:2]
     out, bound = np.zeros(q.shape), np.zeros(q.shape)
+    subnormal = 2.0 ** -35 * (np.abs(v).max(initial=0.0) + 3 * spread.max(initial=0.0))
     for i in range(n):
         see = U.visible(int(pos[i]), length, causal, window, sinks)
         if there is not None:
@@ -37,7 +38,7 @@ def attend_at(q, pos, k, v, causal, window, sinks, scale, spread, there=None):
             out[i, h] = w @ vv
             err = size * (D + 8) * 2.0 ** -23 + (len(s) / 32 + 16) * 2.0 ** -23
             bound[i, h] = 2.0 ** -11 * (w @ sp) + (w * (err + err.max())) @ (np.abs(vv) + 2 * sp) + \
-                len(s) * 2.0 ** -35 * (np.abs(v).max() + 3 * spread.max())
+                len(s) * subnormal
     return out, bound
 
 
